@@ -7,7 +7,8 @@ import sys
 HERE = os.path.dirname(os.path.abspath(__file__))
 SRC = os.path.join(HERE, "csrc", "hymba.cu")
 OUT = os.path.join(HERE, "libhymba.so")
-SOURCES = ["hymba.cu", "common.cuh", "gemm.cuh", "attn.cuh", "ssm.cuh", "misc.cuh"]
+SOURCES = ["hymba.cu", "common.cuh", "gemm.cuh", "attn.cuh", "ssm.cuh", "misc.cuh", "paged.cuh",
+           "paged_api.cuh"]
 
 
 def nvcc_path():

@@ -3,6 +3,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
@@ -10,6 +11,7 @@
 #include <initializer_list>
 #include <mutex>
 #include <string>
+#include <type_traits>
 #include <utility>
 
 #include "../../include/hymba.h"
@@ -17,6 +19,7 @@
 #include "common.cuh"
 #include "gemm.cuh"
 #include "misc.cuh"
+#include "paged.cuh"
 #include "ssm.cuh"
 
 using namespace hymba;
@@ -111,14 +114,14 @@ int device_info(DeviceInfo** out) {
   return HYMBA_OK;
 }
 
-// A 2-D or 3-D tiled map with 128-byte swizzle; dims/strides innermost first, strides in
+// A 2-D to 4-D tiled map with 128-byte swizzle; dims/strides innermost first, strides in
 // bytes for dims 1.. ; box inner extent must be 128 bytes.
 int make_map(CUtensorMap* m, const void* base, CUtensorMapDataType dt, int rank, const uint64_t* dims,
              const uint64_t* strides_bytes, const uint32_t* box,
              CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B) {
   if (!aligned16(base)) return fail(HYMBA_ERR_INVALID_ARG, "tensor base %p not 16-byte aligned", base);
-  cuuint64_t d[3], s[2];
-  cuuint32_t bx[3], es[3] = {1, 1, 1};
+  cuuint64_t d[4], s[3];
+  cuuint32_t bx[4], es[4] = {1, 1, 1, 1};
   for (int i = 0; i < rank; ++i) {
     d[i] = dims[i];
     bx[i] = box[i];
@@ -700,6 +703,8 @@ int check_weights(const hymba_layer_weights* w, const Dims& m, bool need_meta) {
 }
 
 }  // namespace
+
+#include "paged_api.cuh"
 
 // ========================================================================================
 // C ABI

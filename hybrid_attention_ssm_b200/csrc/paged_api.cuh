@@ -1,0 +1,349 @@
+// Host side of the paged key-value cache: argument checks, workspace layout and launches
+// (included by hymba.cu, whose helpers it uses).
+#pragma once
+
+namespace {
+
+constexpr int PAGED_MAX_SELECT_WIDTH = 16384;   // one CTA ranks a sequence's pages in shared memory
+
+struct PagedWs {
+  size_t desc, part, keys, total;
+};
+// The attention's parts and the selection's keys share the space after the status word: each
+// call uses it from its own first kernel on, and calls on one workspace follow one another.
+PagedWs paged_layout(int head_dim, int n_kv_heads, int group, int batch, int max_pages) {
+  PagedWs w;
+  w.desc = 256;
+  w.part = align256(w.desc + (size_t)PA_MAX_GRID * sizeof(int2));
+  w.keys = 256;
+  const size_t attn = w.part + (size_t)PA_MAX_GRID * 2 * group * (head_dim + 2) * 4;
+  const size_t sel = w.keys + (size_t)batch * n_kv_heads * (size_t)max_pages * 8;
+  w.total = align256(attn > sel ? attn : sel);
+  return w;
+}
+
+int check_paged_sizes(const hymba_paged_kv* kv) {
+  if (kv == nullptr) return fail(HYMBA_ERR_INVALID_ARG, "paged cache is NULL");
+  if (kv->dtype != HYMBA_DT_F16 && kv->dtype != HYMBA_DT_BF16)
+    return fail(HYMBA_ERR_UNSUPPORTED, "paged cache type %d (16-bit types only)", kv->dtype);
+  if (kv->head_dim != 64 && kv->head_dim != 128)
+    return fail(HYMBA_ERR_UNSUPPORTED, "paged cache head_dim %d (64 or 128)", kv->head_dim);
+  if (kv->page_size < 16 || kv->page_size > 256 || (kv->page_size & (kv->page_size - 1)))
+    return fail(HYMBA_ERR_UNSUPPORTED, "page_size %d (16, 32, 64, 128 or 256)", kv->page_size);
+  if (kv->n_pages < 1 || kv->n_kv_heads < 1 || kv->n_kv_heads > 1024)
+    return fail(HYMBA_ERR_INVALID_ARG, "paged cache sizes");
+  return HYMBA_OK;
+}
+// Rows, heads and pages by ascending stride, the order a tensor map wants its dimensions in.
+struct PagedDims {
+  long long stride[3];
+  int size[3], box[3];
+  int at_row, at_head;   // their places, 0..2
+};
+PagedDims paged_dims(const hymba_paged_kv* kv) {
+  const long long s[3] = {kv->row_stride, kv->head_stride, kv->page_stride};
+  const int n[3] = {kv->page_size, kv->n_kv_heads, kv->n_pages};
+  int idx[3] = {0, 1, 2};
+  std::stable_sort(idx, idx + 3, [&](int a, int b) { return s[a] < s[b]; });
+  PagedDims r;
+  for (int i = 0; i < 3; ++i) {
+    r.stride[i] = s[idx[i]];
+    r.size[i] = n[idx[i]];
+    r.box[i] = idx[i] == 0 ? std::min(kv->page_size, PA_KT) : 1;
+    if (idx[i] == 0) r.at_row = i;
+    if (idx[i] == 1) r.at_head = i;
+  }
+  return r;
+}
+int check_paged(const hymba_paged_kv* kv, bool need_kv) {
+  HY_TRY(check_paged_sizes(kv));
+  if (need_kv) {
+    if (kv->k == nullptr || kv->v == nullptr || !aligned16(kv->k) || !aligned16(kv->v))
+      return fail(HYMBA_ERR_INVALID_ARG, "paged cache k/v NULL or not 16-byte aligned");
+    // every row is a 16-byte aligned run of head_dim elements (TMA boxes, 8-byte stores)
+    const long long strides[3] = {kv->page_stride, kv->head_stride, kv->row_stride};
+    for (long long s : strides)
+      if (s < kv->head_dim || s % 8 || s >= (1LL << 38))
+        return fail(HYMBA_ERR_INVALID_ARG, "paged cache stride %lld (a multiple of 8, at least head_dim)", s);
+    const PagedDims o = paged_dims(kv);
+    if (o.stride[1] % o.stride[0] || o.stride[2] % o.stride[1])
+      return fail(HYMBA_ERR_INVALID_ARG, "paged cache strides: each must be a multiple of the next smaller one");
+  }
+  if ((kv->k_lo == nullptr) != (kv->k_hi == nullptr) || !aligned16(kv->k_lo) || !aligned16(kv->k_hi))
+    return fail(HYMBA_ERR_INVALID_ARG, "page bounds: both or neither, 16-byte aligned");
+  return HYMBA_OK;
+}
+int check_table(const hymba_page_table* t) {
+  if (t == nullptr || t->pages == nullptr || (reinterpret_cast<uintptr_t>(t->pages) & 3u) || t->batch < 1 ||
+      t->batch > (1 << 20) || t->width < 1 || t->stride < t->width)
+    return fail(HYMBA_ERR_INVALID_ARG, "page table (NULL, misaligned, or sizes)");
+  return HYMBA_OK;
+}
+int check_paged_ws(const void* ws, size_t ws_bytes, size_t need) {
+  if (ws == nullptr || (reinterpret_cast<uintptr_t>(ws) & 255u)) return fail(HYMBA_ERR_INVALID_ARG, "workspace");
+  if (ws_bytes < need) return fail(HYMBA_ERR_WORKSPACE, "workspace %zu < %zu bytes", ws_bytes, need);
+  return HYMBA_OK;
+}
+inline bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+inline int log2_int(int v) {
+  int l = 0;
+  while ((1 << l) < v) ++l;
+  return l;
+}
+
+// kernel launch by the pool's type and head_dim: F is a functor template over (type, D)
+template <typename F>
+int paged_dispatch(const hymba_paged_kv* kv, F&& f) {
+  if (kv->dtype == HYMBA_DT_F16) {
+    if (kv->head_dim == 64) return f(__half{}, std::integral_constant<int, 64>{});
+    return f(__half{}, std::integral_constant<int, 128>{});
+  }
+  if (kv->head_dim == 64) return f(__nv_bfloat16{}, std::integral_constant<int, 64>{});
+  return f(__nv_bfloat16{}, std::integral_constant<int, 128>{});
+}
+
+// Enqueue the append kernel; p holds everything but the pool's fields.
+int launch_paged_append(const hymba_paged_kv* kv, PagedAppendParams& p, float rope_base, cudaStream_t st) {
+  p.Hkv = kv->n_kv_heads;
+  p.n_pages = kv->n_pages;
+  p.ps_log2 = log2_int(kv->page_size);
+  p.page_stride = kv->page_stride;
+  p.head_stride = kv->head_stride;
+  p.row_stride = kv->row_stride;
+  if (p.k != nullptr) {
+    p.pk = kv->k;
+    p.pv = kv->v;
+    p.k_lo = kv->k_lo;
+    p.k_hi = kv->k_hi;
+  }
+  p.rotate = rope_base > 0.f ? 1 : 0;
+  const int h2 = kv->head_dim / 2;
+  for (int j = 0; p.rotate && j < h2; ++j)
+    p.turns[j] = std::pow((double)rope_base, -(double)j / h2) * 0.15915494309189535;
+  // the most runs there can be: a sequence of n tokens touches at most (n + 2 ps - 2) / ps
+  // pages, and no more than it has tokens
+  long long runs = p.B;
+  if (p.cu_new != nullptr) {
+    runs = ((long long)p.T + (long long)p.B * (2 * kv->page_size - 2)) / kv->page_size;
+    if (runs > p.T) runs = p.T;
+  }
+  return paged_dispatch(kv, [&](auto e, auto d) {
+    prof_begin("paged_append", st);
+    HY_CUDA(launch_pdl(paged_append_kernel<decltype(e), decltype(d)::value>, dim3((unsigned)runs, kv->n_kv_heads),
+                       dim3(PAP_THREADS), 0, st, p));
+    prof_end(st);
+    return (int)HYMBA_OK;
+  });
+}
+
+template <typename E, int D, int NHB>
+int launch_paged_attn_inst(const CUtensorMap& mk, const CUtensorMap& mv, const PagedAttnParams& p, int sms,
+                           cudaStream_t st) {
+  using S = PaShape<D, NHB>;
+  static bool attr[64] = {false};
+  int d = 0;
+  HY_CUDA(cudaGetDevice(&d));
+  auto kern = paged_attn_kernel<E, D, NHB>;
+  if (!attr[d & 63]) {
+    HY_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM));
+    attr[d & 63] = true;
+  }
+  const int grid = std::min(sms * S::PER_SM, PA_MAX_GRID);
+  prof_begin("paged_attn", st);
+  HY_CUDA(launch_pdl(kern, dim3(grid), dim3(PA_THREADS), S::SMEM, st, mk, mv, p));
+  prof_end(st);
+  prof_begin("paged_attn_join", st);
+  HY_CUDA(launch_pdl(paged_attn_join_kernel<D>, dim3(grid, p.G), dim3(PJ_THREADS), 0, st, p));
+  prof_end(st);
+  return HYMBA_OK;
+}
+
+// Enqueue the attention over a pool; p holds everything but the pool's and the workspace's fields.
+int launch_paged_attn(const hymba_paged_kv* kv, PagedAttnParams& p, uint8_t* ws, const PagedWs& L, int sms,
+                      cudaStream_t st) {
+  p.Hkv = kv->n_kv_heads;
+  p.n_pages = kv->n_pages;
+  p.ps_log2 = log2_int(kv->page_size);
+  p.desc = reinterpret_cast<int2*>(ws + L.desc);
+  p.part = reinterpret_cast<float*>(ws + L.part);
+  CUtensorMap mk, mv;
+  const PagedDims o = paged_dims(kv);
+  p.dim_row = o.at_row + 1;
+  p.dim_head = o.at_head + 1;
+  const uint64_t dims[4] = {(uint64_t)kv->head_dim, (uint64_t)o.size[0], (uint64_t)o.size[1], (uint64_t)o.size[2]};
+  const uint64_t str[3] = {(uint64_t)o.stride[0] * 2, (uint64_t)o.stride[1] * 2, (uint64_t)o.stride[2] * 2};
+  const uint32_t box[4] = {64, (uint32_t)o.box[0], (uint32_t)o.box[1], (uint32_t)o.box[2]};
+  const CUtensorMapDataType dt =
+      kv->dtype == HYMBA_DT_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  HY_TRY(make_map(&mk, kv->k, dt, 4, dims, str, box));
+  HY_TRY(make_map(&mv, kv->v, dt, 4, dims, str, box));
+  return paged_dispatch(kv, [&](auto e, auto d) {
+    using E = decltype(e);
+    constexpr int D = decltype(d)::value;
+    return p.G <= 8 ? launch_paged_attn_inst<E, D, 1>(mk, mv, p, sms, st)
+                    : launch_paged_attn_inst<E, D, 2>(mk, mv, p, sms, st);
+  });
+}
+
+int paged_group(const hymba_paged_kv* kv, int n_q_heads, int* group) {
+  if (n_q_heads < 1 || n_q_heads % kv->n_kv_heads || n_q_heads / kv->n_kv_heads > 16)
+    return fail(HYMBA_ERR_UNSUPPORTED, "%d query heads over %d KV heads (1 to 16 per KV head)", n_q_heads,
+                kv->n_kv_heads);
+  *group = n_q_heads / kv->n_kv_heads;
+  return HYMBA_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int hymba_paged_workspace_size(const hymba_paged_kv* kv, int batch, int n_q_heads, int max_pages, size_t* bytes) {
+  HY_TRY(check_paged_sizes(kv));
+  int G = 0;
+  HY_TRY(paged_group(kv, n_q_heads, &G));
+  if (bytes == nullptr || batch < 1 || max_pages < 1) return fail(HYMBA_ERR_INVALID_ARG, "paged workspace arguments");
+  *bytes = paged_layout(kv->head_dim, kv->n_kv_heads, G, batch, max_pages).total;
+  return HYMBA_OK;
+}
+
+int hymba_paged_append(const hymba_paged_kv* kv, const hymba_page_table* table, const int* start, const int* cu_new,
+                       int n_tokens, int src_dtype, const void* k, long long k_stride, const void* v,
+                       long long v_stride, const void* q, long long q_stride, int n_q_heads, void* q_out,
+                       float rope_base, void* ws, size_t ws_bytes, hymba_stream stream) {
+  const bool has_kv = k != nullptr;
+  HY_TRY(check_paged(kv, has_kv));
+  HY_TRY(check_table(table));
+  HY_TRY(check_paged_ws(ws, ws_bytes, 256));
+  if (src_dtype != HYMBA_DT_F32 && src_dtype != HYMBA_DT_BF16 && src_dtype != HYMBA_DT_F16)
+    return fail(HYMBA_ERR_UNSUPPORTED, "source type %d", src_dtype);
+  if (start == nullptr || !aligned4(start) || !aligned4(cu_new)) return fail(HYMBA_ERR_INVALID_ARG, "start / cu_new");
+  if (n_tokens < 0 || (cu_new == nullptr && n_tokens != table->batch))
+    return fail(HYMBA_ERR_INVALID_ARG, "n_tokens %d for a batch of %d", n_tokens, table->batch);
+  if (has_kv != (v != nullptr)) return fail(HYMBA_ERR_INVALID_ARG, "k and v: both or neither");
+  if ((q == nullptr) != (q_out == nullptr)) return fail(HYMBA_ERR_INVALID_ARG, "q and q_out: both or neither");
+  if (!has_kv && q == nullptr) return fail(HYMBA_ERR_INVALID_ARG, "neither keys nor queries");
+  if (!(rope_base >= 0.f) || std::isinf(rope_base)) return fail(HYMBA_ERR_INVALID_ARG, "rope_base %g", rope_base);
+  const int vec = src_dtype == HYMBA_DT_F32 ? 4 : 8;   // 16 bytes
+  int G = 1;
+  if (q != nullptr) HY_TRY(paged_group(kv, n_q_heads, &G));
+  struct { const void* p; long long s; long long w; const char* n; } rows[3] = {
+      {k, k_stride, (long long)kv->n_kv_heads * kv->head_dim, "k"},
+      {v, v_stride, (long long)kv->n_kv_heads * kv->head_dim, "v"},
+      {q, q_stride, (long long)G * kv->n_kv_heads * kv->head_dim, "q"}};
+  for (const auto& r : rows)
+    if (r.p != nullptr && (!aligned16(r.p) || r.s < r.w || r.s % vec))
+      return fail(HYMBA_ERR_INVALID_ARG, "%s rows: not 16-byte aligned, or stride %lld", r.n, r.s);
+  if (!aligned16(q_out)) return fail(HYMBA_ERR_INVALID_ARG, "q_out not 16-byte aligned");
+  DeviceInfo* dev = nullptr;
+  HY_TRY(device_info(&dev));
+  if (n_tokens == 0) return HYMBA_OK;
+  PagedAppendParams p{};
+  p.q = q; p.k = k; p.v = v;
+  p.q_stride = q_stride; p.k_stride = k_stride; p.v_stride = v_stride;
+  p.src = src_dtype;
+  p.n_slices = 1;
+  p.q_out = q_out;
+  p.start = start;
+  p.cu_new = cu_new;
+  p.table = table->pages; p.table_stride = table->stride; p.width = table->width;
+  p.B = table->batch; p.T = n_tokens; p.G = G;
+  p.status = reinterpret_cast<DevStatus*>(ws);
+  return launch_paged_append(kv, p, rope_base, (cudaStream_t)stream);
+}
+
+int hymba_paged_select(const hymba_paged_kv* kv, const hymba_page_table* table, const int* seq_lens, const void* q,
+                       long long q_stride, int n_q_heads, int n_first, int n_last, int top_pages, int* page_idx,
+                       void* ws, size_t ws_bytes, hymba_stream stream) {
+  HY_TRY(check_paged(kv, false));
+  HY_TRY(check_table(table));
+  int G = 0;
+  HY_TRY(paged_group(kv, n_q_heads, &G));
+  if (kv->k_lo == nullptr) return fail(HYMBA_ERR_INVALID_ARG, "page selection needs the cache's page bounds");
+  if (table->width > PAGED_MAX_SELECT_WIDTH)
+    return fail(HYMBA_ERR_UNSUPPORTED, "page selection over %d pages (at most %d)", table->width,
+                PAGED_MAX_SELECT_WIDTH);
+  if (seq_lens == nullptr || !aligned4(seq_lens) || page_idx == nullptr || !aligned4(page_idx) || q == nullptr ||
+      !aligned16(q) || q_stride < (long long)n_q_heads * kv->head_dim || q_stride % 8)
+    return fail(HYMBA_ERR_INVALID_ARG, "seq_lens / page_idx / q");
+  if (n_first < 0 || n_last < 0 || top_pages < 1 || (long long)n_first + n_last > top_pages)
+    return fail(HYMBA_ERR_INVALID_ARG, "top_pages %d with %d first and %d last", top_pages, n_first, n_last);
+  const PagedWs L = paged_layout(kv->head_dim, kv->n_kv_heads, G, table->batch, table->width);
+  HY_TRY(check_paged_ws(ws, ws_bytes, L.total));
+  DeviceInfo* dev = nullptr;
+  HY_TRY(device_info(&dev));
+  cudaStream_t st = (cudaStream_t)stream;
+  uint8_t* wsb = static_cast<uint8_t*>(ws);
+  PagedSelectParams p{};
+  p.k_lo = kv->k_lo; p.k_hi = kv->k_hi;
+  p.q = q; p.q_stride = q_stride;
+  p.table = table->pages; p.table_stride = table->stride; p.width = table->width;
+  p.lens = seq_lens;
+  p.B = table->batch; p.Hkv = kv->n_kv_heads; p.G = G; p.n_pages = kv->n_pages;
+  p.ps_log2 = log2_int(kv->page_size);
+  p.n_first = n_first; p.n_last = n_last; p.top = top_pages;
+  p.keys = reinterpret_cast<unsigned long long*>(wsb + L.keys);
+  p.page_idx = page_idx;
+  p.status = reinterpret_cast<DevStatus*>(ws);
+  const long long warps = (long long)p.B * p.Hkv * cdiv(p.width, PSC_PAGES);
+  const long long blocks = (warps + PSC_THREADS / 32 - 1) / (PSC_THREADS / 32);
+  if (blocks > 0x7fffffff || (long long)p.B * p.Hkv > 0x7fffffff) return fail(HYMBA_ERR_UNSUPPORTED, "batch too large");
+  HY_TRY(paged_dispatch(kv, [&](auto e, auto d) {
+    prof_begin("paged_score", st);
+    HY_CUDA(launch_pdl(paged_score_kernel<decltype(e), decltype(d)::value>, dim3((unsigned)blocks), dim3(PSC_THREADS),
+                       0, st, p));
+    prof_end(st);
+    return (int)HYMBA_OK;
+  }));
+  static bool attr[64] = {false};
+  int dcur = 0;
+  HY_CUDA(cudaGetDevice(&dcur));
+  if (!attr[dcur & 63]) {
+    HY_CUDA(cudaFuncSetAttribute(paged_pick_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 PAGED_MAX_SELECT_WIDTH * 8));
+    attr[dcur & 63] = true;
+  }
+  prof_begin("paged_pick", st);
+  HY_CUDA(launch_pdl(paged_pick_kernel, dim3(p.B * p.Hkv), dim3(PPK_THREADS), (size_t)p.width * 8, st, p));
+  prof_end(st);
+  return HYMBA_OK;
+}
+
+int hymba_paged_attention(const hymba_paged_kv* kv, const hymba_page_table* table, const int* seq_lens, const void* q,
+                          long long q_stride, int n_q_heads, float scale, int n_meta, int window, const int* page_idx,
+                          int top_pages, void* out, int out_dtype, long long out_stride, float* lse, void* ws,
+                          size_t ws_bytes, hymba_stream stream) {
+  HY_TRY(check_paged(kv, true));
+  HY_TRY(check_table(table));
+  int G = 0;
+  HY_TRY(paged_group(kv, n_q_heads, &G));
+  const long long width = (long long)n_q_heads * kv->head_dim;
+  if (seq_lens == nullptr || !aligned4(seq_lens) || q == nullptr || !aligned16(q) || q_stride < width || q_stride % 8)
+    return fail(HYMBA_ERR_INVALID_ARG, "seq_lens / q");
+  if (out_dtype != HYMBA_DT_F32 && out_dtype != HYMBA_DT_BF16 && out_dtype != HYMBA_DT_F16)
+    return fail(HYMBA_ERR_UNSUPPORTED, "output type %d", out_dtype);
+  if (out == nullptr || !aligned16(out) || out_stride < width || out_stride % 8 || !aligned4(lse))
+    return fail(HYMBA_ERR_INVALID_ARG, "out / lse");
+  if (!std::isfinite(scale)) return fail(HYMBA_ERR_INVALID_ARG, "scale %g", scale);
+  if (n_meta < 0 || window < 0 || (window == 0 && n_meta > 0))
+    return fail(HYMBA_ERR_INVALID_ARG, "n_meta %d, window %d (meta tokens go with a window)", n_meta, window);
+  if (page_idx != nullptr && (window > 0 || top_pages < 1 || !aligned4(page_idx)))
+    return fail(HYMBA_ERR_INVALID_ARG, "a page list goes without a window, with top_pages >= 1");
+  const PagedWs L = paged_layout(kv->head_dim, kv->n_kv_heads, G, 1, 1);
+  HY_TRY(check_paged_ws(ws, ws_bytes, L.total));
+  DeviceInfo* dev = nullptr;
+  HY_TRY(device_info(&dev));
+  PagedAttnParams p{};
+  p.q = q; p.q_stride = q_stride;
+  p.out = out; p.out_dt = out_dtype; p.out_stride = out_stride;
+  p.lse = lse;
+  p.table = table->pages; p.table_stride = table->stride; p.width = table->width;
+  p.lens = seq_lens;
+  p.page_idx = page_idx; p.top = top_pages;
+  p.B = table->batch; p.Hq = n_q_heads; p.G = G;
+  p.M = n_meta; p.W = window;
+  p.scale_log2 = scale * 1.4426950408889634f;
+  p.status = reinterpret_cast<DevStatus*>(ws);
+  return launch_paged_attn(kv, p, static_cast<uint8_t*>(ws), L, dev->sms, (cudaStream_t)stream);
+}
+
+}  // extern "C"

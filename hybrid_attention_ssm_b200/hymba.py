@@ -20,6 +20,7 @@ OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_WORKSPACE, ERR_CUDA, ERR_TIMEOUT, ERR_
 KV_OWN, KV_PRODUCER, KV_CONSUMER = 0, 1, 2
 CACHE_SWA, CACHE_GLOBAL = 0, 1
 MODE_PREFILL, MODE_DECODE, MODE_PREFILL_HOST = 0, 1, 2
+DT_F32, DT_BF16, DT_F16 = 0, 1, 2
 
 _c_int, _c_size, _vp = ctypes.c_int, ctypes.c_size_t, ctypes.c_void_p
 
@@ -66,6 +67,16 @@ class DecodeStageLayout(ctypes.Structure):
     _fields_ = [(n, _c_size) for n in ("proj", "xc", "xbc_part", "y")] + \
                [("proj_slice_stride", ctypes.c_longlong), ("xbc_slice_stride", ctypes.c_longlong)] + \
                [(n, _c_int) for n in ("in_split", "xproj_split", "ld_proj", "ld_xbc")]
+
+
+class PagedKV(ctypes.Structure):
+    _fields_ = [(n, _c_int) for n in ("dtype", "n_pages", "page_size", "n_kv_heads", "head_dim")] + \
+               [(n, ctypes.c_longlong) for n in ("page_stride", "head_stride", "row_stride")] + \
+               [(n, _vp) for n in ("k", "v", "k_lo", "k_hi")]
+
+
+class PageTable(ctypes.Structure):
+    _fields_ = [("pages", _vp), ("batch", _c_int), ("width", _c_int), ("stride", ctypes.c_longlong)]
 
 
 _LIB = None
@@ -129,6 +140,16 @@ def lib():
             "hymba_ffn_workspace_size": ([_c_int, _c_int, _c_int, ctypes.POINTER(_c_size)], _c_int),
             "hymba_ffn_swiglu_decode": ([_vp, _vp, _vp, _c_int, _c_int, _c_int, _vp, _vp, _vp, _c_size, _vp], _c_int),
             "hymba_l2_prefetch": ([ctypes.POINTER(_vp), ctypes.POINTER(_c_size), _c_int, _vp], _c_int),
+            "hymba_paged_workspace_size": ([ctypes.POINTER(PagedKV), _c_int, _c_int, _c_int,
+                                            ctypes.POINTER(_c_size)], _c_int),
+            "hymba_paged_append": ([ctypes.POINTER(PagedKV), ctypes.POINTER(PageTable), _vp, _vp, _c_int, _c_int,
+                                    _vp, ctypes.c_longlong, _vp, ctypes.c_longlong, _vp, ctypes.c_longlong, _c_int,
+                                    _vp, ctypes.c_float, _vp, _c_size, _vp], _c_int),
+            "hymba_paged_select": ([ctypes.POINTER(PagedKV), ctypes.POINTER(PageTable), _vp, _vp, ctypes.c_longlong,
+                                    _c_int, _c_int, _c_int, _c_int, _vp, _vp, _c_size, _vp], _c_int),
+            "hymba_paged_attention": ([ctypes.POINTER(PagedKV), ctypes.POINTER(PageTable), _vp, _vp,
+                                       ctypes.c_longlong, _c_int, ctypes.c_float, _c_int, _c_int, _vp, _c_int, _vp,
+                                       _c_int, ctypes.c_longlong, _vp, _vp, _c_size, _vp], _c_int),
             "hymba_set_wait_limit_ns": ([ctypes.c_ulonglong], _c_int),
             "hymba_prepend_meta": ([_vp, _vp, _c_int, _c_int, _c_int, _c_int, _vp, _vp], _c_int),
             "hymba_selftest_wait_timeout": ([_vp, _c_size, _vp], _c_int),
@@ -219,6 +240,159 @@ class Cache:
         g = lambda n: ptr(self.t[n]) if n in self.t else None
         self.c = KVCache(kind, batch, Hkv, D, dims.n_meta, dims.window, max_tokens,
                          g("meta_k"), g("meta_v"), g("ring_k"), g("ring_v"), g("k"), g("v"))
+
+
+_DT_CODE = {torch.float32: DT_F32, torch.bfloat16: DT_BF16, torch.float16: DT_F16}
+
+
+class PagedCache:
+    """A paged key-value cache: a pool of pages owned by torch tensors, shared by all sequences.
+
+    k, v        [n_pages, Hkv, page_size, D] fp16 or bf16, head_dim innermost and contiguous (a
+                pool stored in another order of pages, heads and rows is passed as a permuted view)
+    k_lo, k_hi  [n_pages, Hkv, D] contiguous, the page bounds that paged_append keeps and
+                paged_select reads; optional
+    """
+
+    def __init__(self, k, v, k_lo=None, k_hi=None):
+        _refuse_unless(k.dim() == 4 and k.shape == v.shape and k.dtype == v.dtype and k.stride() == v.stride(),
+                       "paged cache: k and v must be [n_pages, Hkv, page_size, D] of one type and layout")
+        _refuse_unless(k.stride(3) == 1, "paged cache: head_dim must be contiguous")
+        n, hkv, ps, D = k.shape
+        for t in (k_lo, k_hi):
+            _refuse_unless(t is None or (tuple(t.shape) == (n, hkv, D) and t.dtype == k.dtype and t.is_contiguous()),
+                           "page bounds must be contiguous [n_pages, Hkv, D] in the pool's type")
+        _one_device(k, v, k_lo, k_hi)
+        self.t = {"k": k, "v": v, "k_lo": k_lo, "k_hi": k_hi}
+        self.c = PagedKV(_DT_CODE.get(k.dtype, -1), n, ps, hkv, D, k.stride(0), k.stride(1), k.stride(2), ptr(k),
+                         ptr(v), ptr(k_lo), ptr(k_hi))
+
+    @classmethod
+    def zeros(cls, n_pages, page_size, n_kv_heads, head_dim, dtype=torch.float16, bounds=False, device="cuda"):
+        z = lambda *s: torch.zeros(*s, dtype=dtype, device=device)
+        kv = [z(n_pages, n_kv_heads, page_size, head_dim) for _ in range(2)]
+        return cls(*kv, *[z(n_pages, n_kv_heads, head_dim) for _ in range(2 if bounds else 0)])
+
+
+def _refuse_unless(ok, msg):
+    if not ok:
+        raise HymbaError(ERR_INVALID_ARG, msg)
+
+
+def _one_device(*tensors):
+    """The library launches on the current device: every tensor must live there."""
+    dev = {t.device for t in tensors if t is not None}
+    _refuse_unless(len(dev) == 1 and next(iter(dev)).type == "cuda", f"tensors must be on one CUDA device, got {dev}")
+    _refuse_unless(next(iter(dev)).index == torch.cuda.current_device(),
+                   f"tensors on {next(iter(dev))}, but the current device is cuda:{torch.cuda.current_device()}")
+
+
+def _page_table(table):
+    _refuse_unless(table.dim() == 2 and table.dtype == torch.int32 and table.stride(1) == 1,
+                   "block table must be int32 [batch, width] with contiguous rows")
+    # (a single row's stride is whatever torch made it)
+    stride = table.shape[1] if table.shape[0] == 1 else table.stride(0)
+    return PageTable(ptr(table), table.shape[0], table.shape[1], stride)
+
+
+def _int32_vector(t, n, name):
+    _refuse_unless(t.dtype == torch.int32 and t.dim() == 1 and t.shape[0] == n and t.is_contiguous(),
+                   f"{name} must be a contiguous int32 vector of {n}")
+
+
+def _head_rows(t, D, name):
+    """Row stride of [rows, heads, D] whose heads are contiguous."""
+    _refuse_unless(t.dim() == 3 and t.shape[2] == D and t.stride(2) == 1 and (t.shape[1] == 1 or t.stride(1) == D),
+                   f"{name} must be [rows, heads, {D}] with contiguous heads")
+    return t.shape[1] * D if t.shape[0] <= 1 else t.stride(0)
+
+
+def paged_workspace_size(cache: PagedCache, batch, n_q_heads, max_pages) -> int:
+    """Workspace bytes for paged_select and paged_attention (max_pages: the block table's width)."""
+    n = ctypes.c_size_t()
+    check(lib().hymba_paged_workspace_size(ctypes.byref(cache.c), batch, n_q_heads, max_pages, ctypes.byref(n)))
+    return n.value
+
+
+def paged_append(cache: PagedCache, table, start, k, v, ws, q=None, q_out=None, cu_new=None, rope_base=10000.0,
+                 stream=None):
+    """hymba_paged_append: rotate the new tokens' keys k [T, Hkv, D] (and queries q [T, Hq, D] into
+    q_out) to their positions start[b] + i and store k and v in their sequences' pages.
+
+    table [B, width], start [B] int32; cu_new [B + 1] int32 gives each sequence's rows (None: one
+    token per sequence).  k and v may be None together.  rope_base 0: no rotation."""
+    D, Hkv = cache.c.head_dim, cache.c.n_kv_heads
+    src = k if k is not None else q
+    _refuse_unless(src is not None and (k is None) == (v is None) and (q is None) == (q_out is None),
+                   "paged_append: k and v go together, q and q_out go together")
+    _one_device(cache.t["k"], table, start, k, v, ws, q, q_out, cu_new)
+    tb = _page_table(table)
+    _int32_vector(start, tb.batch, "start")
+    if cu_new is not None:
+        _int32_vector(cu_new, tb.batch + 1, "cu_new")
+    T = src.shape[0]
+    strides = [0, 0, 0]
+    for i, (t, heads, name) in enumerate(((k, Hkv, "k"), (v, Hkv, "v"), (q, None, "q"))):
+        if t is not None:
+            strides[i] = _head_rows(t, D, name)
+            _refuse_unless(t.shape[0] == T and t.dtype == src.dtype and (heads is None or t.shape[1] == heads),
+                           f"paged_append: {name} {tuple(t.shape)} {t.dtype}")
+    Hq = q.shape[1] if q is not None else 0
+    if q_out is not None:
+        _refuse_unless(q_out.shape == q.shape and q_out.dtype == cache.t["k"].dtype and q_out.is_contiguous(),
+                       "paged_append: q_out must be contiguous, shaped like q, in the pool's type")
+    check(lib().hymba_paged_append(ctypes.byref(cache.c), ctypes.byref(tb), ptr(start), ptr(cu_new), T,
+                                   _DT_CODE.get(src.dtype, -1), ptr(k), strides[0], ptr(v), strides[1], ptr(q),
+                                   strides[2], Hq, ptr(q_out), rope_base, ptr(ws), ws.numel(),
+                                   stream_handle(stream)))
+
+
+def _query_rows(cache, q, batch):
+    _refuse_unless(q.dim() == 3 and q.shape[0] == batch and q.dtype == cache.t["k"].dtype,
+                   "q must be [batch, Hq, D] in the pool's type")
+    return _head_rows(q, cache.c.head_dim, "q")
+
+
+def paged_select(cache: PagedCache, q, table, seq_lens, page_idx, ws, n_first=1, n_last=1, stream=None):
+    """hymba_paged_select: page_idx [B, Hkv, top] int32 receives, per sequence and KV head, the
+    pages (numbers within the sequence, ascending, -1 behind the last) that the rotated query
+    q [B, Hq, D] should read: the first n_first, the last n_last and the best by page bounds."""
+    _one_device(cache.t["k"], q, table, seq_lens, page_idx, ws)
+    tb = _page_table(table)
+    _int32_vector(seq_lens, tb.batch, "seq_lens")
+    qs = _query_rows(cache, q, tb.batch)
+    _refuse_unless(page_idx.dtype == torch.int32 and page_idx.dim() == 3 and page_idx.is_contiguous() and
+                   tuple(page_idx.shape[:2]) == (tb.batch, cache.c.n_kv_heads),
+                   "page_idx must be contiguous int32 [batch, Hkv, top_pages]")
+    check(lib().hymba_paged_select(ctypes.byref(cache.c), ctypes.byref(tb), ptr(seq_lens), ptr(q), qs, q.shape[1],
+                                   n_first, n_last, page_idx.shape[2], ptr(page_idx), ptr(ws), ws.numel(),
+                                   stream_handle(stream)))
+
+
+def paged_attention(cache: PagedCache, q, table, seq_lens, out, ws, scale=None, n_meta=0, window=0, page_idx=None,
+                    lse=None, stream=None):
+    """hymba_paged_attention: out [B, Hq, D] = attention of one (rotated) query per sequence over
+    the first seq_lens[b] positions of its pages; with window > 0 over the first n_meta positions
+    and the last `window`; with page_idx over the listed pages.  scale: 1/sqrt(D) by default."""
+    _one_device(cache.t["k"], q, table, seq_lens, out, ws, page_idx, lse)
+    tb = _page_table(table)
+    _int32_vector(seq_lens, tb.batch, "seq_lens")
+    qs = _query_rows(cache, q, tb.batch)
+    _refuse_unless(out.shape == q.shape, "out must be shaped like q")
+    top = 0
+    if page_idx is not None:
+        _refuse_unless(page_idx.dtype == torch.int32 and page_idx.dim() == 3 and page_idx.is_contiguous() and
+                       tuple(page_idx.shape[:2]) == (tb.batch, cache.c.n_kv_heads),
+                       "page_idx must be contiguous int32 [batch, Hkv, top_pages]")
+        top = page_idx.shape[2]
+    if lse is not None:
+        _refuse_unless(lse.dtype == torch.float32 and tuple(lse.shape) == (tb.batch, q.shape[1]) and
+                       lse.is_contiguous(), "lse must be contiguous fp32 [batch, Hq]")
+    scale = cache.c.head_dim ** -0.5 if scale is None else scale
+    check(lib().hymba_paged_attention(ctypes.byref(cache.c), ctypes.byref(tb), ptr(seq_lens), ptr(q), qs, q.shape[1],
+                                      scale, n_meta, window, ptr(page_idx), top, ptr(out), _DT_CODE.get(out.dtype, -1),
+                                      _head_rows(out, cache.c.head_dim, "out"), ptr(lse), ptr(ws), ws.numel(),
+                                      stream_handle(stream)))
 
 
 def workspace_size(dims, batch, n_tokens, x_has_meta=0, mode=MODE_PREFILL):

@@ -286,6 +286,127 @@ int hymba_mixer_decode_ragged(const hymba_layer_cfg* cfg, const hymba_layer_weig
                               float* ssm_state, float* conv_state, const hymba_bf16* residual, hymba_bf16* out,
                               void* workspace, size_t ws_bytes, hymba_stream stream);
 
+/* ---------------------------------------------------------------------------------------
+ * Paged key-value cache: the attention branch's K and V for serving loops whose sequences
+ * come, grow and go at different lengths.  Instead of one contiguous cache per sequence, all
+ * sequences share a pool of pages of page_size positions; a block table names each
+ * sequence's pages in order, so position p of sequence b is row p % page_size of page
+ * pages[b * stride + p / page_size].  Which pages are free is the caller's bookkeeping; pages
+ * that sequences share (a common prefix) may be read by all of them but must not be appended
+ * to.  The meta tokens are the first n_meta positions of every sequence and, being the same
+ * for all of them, may live in shared pages.
+ * --------------------------------------------------------------------------------------- */
+enum { HYMBA_DT_F32 = 0, HYMBA_DT_BF16 = 1, HYMBA_DT_F16 = 2 };
+
+/* The pool (device pointers).  Element (page, head, row, d) of k and of v is at
+ * page*page_stride + head*head_stride + row*row_stride + d elements: any order of pages,
+ * heads and rows.  [n_pages, Hkv, page_size, D] keeps a page's rows of one head contiguous and
+ * is the fastest to read.
+ * Supported: dtype F16 or BF16 (K stored after RoPE; a cache of normalised-input layers
+ * wants F16, which rounds 8x finer), head_dim 64 or 128, page_size 16, 32, 64, 128 or 256,
+ * strides multiples of 8, at least head_dim and each a multiple of the next smaller one, k and
+ * v 16-byte aligned.
+ *   k_lo, k_hi   [n_pages, Hkv, D] in the pool's type, contiguous, or both NULL: the page
+ *                bounds, per page and channel the smallest and largest stored key value, which
+ *                hymba_paged_append keeps and hymba_paged_select reads. */
+typedef struct hymba_paged_kv {
+  int dtype;
+  int n_pages;
+  int page_size;
+  int n_kv_heads;
+  int head_dim;
+  long long page_stride, head_stride, row_stride;   /* elements, for k and for v */
+  void* k;
+  void* v;
+  void* k_lo;
+  void* k_hi;
+} hymba_paged_kv;
+
+/* A batch's block table: pages [batch] rows of `width` int32 page numbers, `stride` apart
+ * (device).  Entries behind a sequence's last page are never read.  An entry outside
+ * 0..n_pages-1 where a page is needed is recorded in the status word
+ * (HYMBA_ERR_INVALID_ARG from hymba_status_read); nothing is read or written through it. */
+typedef struct hymba_page_table {
+  const int* pages;
+  int batch;
+  int width;
+  long long stride;
+} hymba_page_table;
+
+/* Bytes of workspace that hymba_paged_select and hymba_paged_attention need for up to `batch`
+ * sequences of up to max_pages pages each (the table's width).  One workspace serves all the
+ * paged calls, one after another; calls that may overlap on the GPU need one each. */
+int hymba_paged_workspace_size(const hymba_paged_kv* kv, int batch, int n_q_heads, int max_pages, size_t* bytes);
+
+/* Append new tokens: rotate (RoPE, half-split pairs, angle position * base^(-2j/D)) and store.
+ * Sequence b's i-th new token has position start[b] + i.  Its key (rotated) and value go to
+ * its page, rounded once to the pool's type; its query (rotated, rounded the same way) goes to
+ * q_out.
+ *   start     int32 [batch] (device): positions already in the cache
+ *   cu_new    int32 [batch + 1] (device), ascending from 0: sequence b's tokens are rows
+ *             cu_new[b] .. cu_new[b+1]-1; rows from cu_new[batch] on are left alone.  NULL: one
+ *             token per sequence (n_tokens == batch)
+ *   n_tokens  rows of k, v, q (an upper bound when cu_new is given)
+ *   k, v, q   rows of src_dtype (F32, BF16 or F16), heads contiguous, k_stride / v_stride /
+ *             q_stride elements apart (column slices of a fused projection): 16-byte aligned,
+ *             strides multiples of 16 bytes.  k and v may be NULL together (only queries are
+ *             rotated: a layer that reads another layer's cache), q and q_out likewise
+ *   q_out     [n_tokens, Hq, D] in the pool's type
+ *   rope_base 0: no rotation (keys that were rotated before, e.g. a prefill cache's)
+ * Page bounds, when the cache has them: a page whose row 0 is written in this call starts
+ * over; otherwise the new keys widen its bounds.
+ * Recorded in the status word (HYMBA_ERR_INVALID_ARG): a cu_new entry outside the rows or
+ * descending, a negative or too large start (that sequence is skipped), a position beyond the
+ * table or a bad page (its keys and values are not stored); HYMBA_ERR_FP16_RANGE: a value that
+ * an F16 pool cannot hold.
+ * Two sequences that append to the same page race. */
+int hymba_paged_append(const hymba_paged_kv* kv, const hymba_page_table* table, const int* start, const int* cu_new,
+                       int n_tokens, int src_dtype, const void* k, long long k_stride, const void* v,
+                       long long v_stride, const void* q, long long q_stride, int n_q_heads, void* q_out,
+                       float rope_base, void* workspace, size_t ws_bytes, hymba_stream stream);
+
+/* Choose the pages a decode query reads: for every sequence and KV head the first n_first
+ * pages (they hold the meta tokens), the last n_last (the newest tokens), and of the others
+ * those with the largest
+ *   score(page) = sum over the group's query heads of max { q . k : k_lo <= k <= k_hi },
+ * top_pages in all, ties to the lower page number.  Scores are held in 64 bits, so the choice
+ * does not depend on rounding.
+ *   seq_lens  int32 [batch] (device): positions in the cache, the new token's included
+ *   q         [batch] rows of n_q_heads * D in the pool's type, q_stride apart, rotated
+ *   page_idx  int32 [batch, Hkv, top_pages] (device, output): numbers within the sequence,
+ *             ascending, -1 behind the last one.  A sequence of at most top_pages pages gets
+ *             all of them.
+ * Needs page bounds.  n_first + n_last <= top_pages; table width <= 16384 (UNSUPPORTED above).
+ * A length that is negative or beyond the table is recorded (HYMBA_ERR_INVALID_ARG) and
+ * clamped; a page that is not in the pool is recorded and ranks last. */
+int hymba_paged_select(const hymba_paged_kv* kv, const hymba_page_table* table, const int* seq_lens, const void* q,
+                       long long q_stride, int n_q_heads, int n_first, int n_last, int top_pages, int* page_idx,
+                       void* workspace, size_t ws_bytes, hymba_stream stream);
+
+/* Attention of one new token per sequence ([JJ] eq. (1)) over its pages:
+ *   out[b, h] = sum_j softmax_j(scale * q[b, h] . k_j) v_j,   KV head h * Hkv / Hq,
+ * over positions j < seq_lens[b] (the new token is appended first) that are visible:
+ *   window 0, page_idx NULL   all of them
+ *   window W > 0              j < n_meta or j >= seq_lens[b] - W
+ *   page_idx                  those of the listed pages (int32 [batch, Hkv, top_pages], as
+ *                             hymba_paged_select writes them: the first min(top_pages, pages of
+ *                             the sequence) entries are read, entries that are no page of the
+ *                             sequence are skipped, an entry listed twice counts twice)
+ * A sequence with no visible position gets zeros.  Values and keys at positions that are not
+ * visible, NaN included, have no influence.
+ *   q    rows of n_q_heads * D in the pool's type (n_q_heads up to 16 per KV head), q_stride
+ *        apart (a multiple of 8); out likewise in out_dtype (F32, BF16 or F16), rounded once
+ *   lse  [batch, n_q_heads] fp32, or NULL: log(sum_j exp(scale * q.k_j)), -inf for no position
+ * Scores, probabilities and sums are fp32; the products with V take the probabilities as two
+ * 16-bit halves.  The result does not depend on scheduling.  Work is shared out on the
+ * device from seq_lens, so a captured call serves any later lengths that the table can hold.
+ * A length that is negative or beyond the table is recorded (HYMBA_ERR_INVALID_ARG) and
+ * clamped; the positions of a page that is not in the pool are recorded and skipped. */
+int hymba_paged_attention(const hymba_paged_kv* kv, const hymba_page_table* table, const int* seq_lens, const void* q,
+                          long long q_stride, int n_q_heads, float scale, int n_meta, int window, const int* page_idx,
+                          int top_pages, void* out, int out_dtype, long long out_stride, float* lse, void* workspace,
+                          size_t ws_bytes, hymba_stream stream);
+
 /* Byte offsets, inside a prefill workspace, of the stage buffers of the last prefill (for
  * stage-by-stage checks).  Layouts (rows r = b*T + t):
  *   q      [B*T, Hq*D]  fp16  queries after RoPE
