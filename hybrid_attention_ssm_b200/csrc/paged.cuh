@@ -606,37 +606,43 @@ __global__ void __launch_bounds__(PPK_THREADS) paged_pick_kernel(const PagedSele
 // over the visible positions j < lens[b]: all of them, those with j < M or j >= lens[b] - W
 // (meta tokens and window), or those of the listed pages.
 //
-// The keys of (sequence, kv head) are cut into tiles of 64 positions, and the tiles of all of
-// them, in order, are dealt to the CTAs as equal contiguous shares: a long sequence is split
-// over many CTAs and short ones share one, whatever the lengths are (they are known on the
-// device only, and a replayed graph sees new ones).  A (sequence, head) that one CTA covers
-// alone is finished there; of one that is cut, each CTA leaves its running maximum, sum and
-// weighted values, which paged_attn_join_kernel merges in CTA order.  A CTA has at most two
-// such parts: one that an earlier CTA began and one that a later CTA ends.
+// The keys of (sequence, kv head), an item, are cut into tiles of 64 positions, and the tiles
+// of all items, in order, are dealt to the CTAs (one per SM) as equal contiguous shares, and
+// a CTA's share to its groups: a long sequence is split over many CTAs and short ones share a
+// group, whatever the lengths are (they are known on the device only, and a replayed graph
+// sees new ones).  An item that one group covers alone is finished there.  Of a cut item every
+// group leaves its running maximum, sum and weighted values in shared memory; when the CTA's
+// groups are done it merges the parts of the same item, and if other CTAs have a share of the
+// item too it leaves one part in the workspace and counts it, and the CTA that completes the
+// count merges the parts in CTA order: the result does not depend on which one that is.  One
+// CTA per SM (instead of three small ones) keeps that last join to at most 148 parts and gives
+// it all of the CTA's threads.
 //
-// A producer warp walks the share: its lanes look up the pages and issue one TMA box per page
+// A group is a producer warp and four consumer warps with a ring of stages of their own.  The
+// producer walks the group's tiles: its lanes look up the pages and issue one TMA box per page
 // piece (128-byte swizzled rows; D = 128 as two 64-wide halves), with the visibility of the
 // tile's 64 positions as a bit mask beside it; a page that does not exist gets an
-// out-of-range coordinate, which TMA fills with zeros.  Four consumer warps take 16 positions
-// of every tile each.  The group's query heads are rows of 16 x 16 x 8 tensor-core products:
+// out-of-range coordinate, which TMA fills with zeros.  The consumer warps take 16 positions
+// of every tile each.  The item's query heads are rows of 16 x 16 x 8 tensor-core products:
 // rows 0..7 hold up to 8 heads, and rows 8..15, otherwise empty, take in the second product
 // the rounding error of the probabilities (p = hi + lo, both 16 bits), so P V costs the same
 // number of instructions and keeps about twice the mantissa.  With 9 to 16 heads (NHB = 2)
 // rows 8..15 of Q K^T are heads 8..15, and P V runs once per 8 heads.
 // ----------------------------------------------------------------------------------------
 constexpr int PA_KT = 64;
-constexpr int PA_CONSUMERS = 128;
-constexpr int PA_THREADS = PA_CONSUMERS + 32;
-constexpr int PA_MAX_GRID = 148 * 3;   // CTAs of any variant (sizes the workspace)
+constexpr int PA_MAX_GRID = 148;   // CTAs (sizes the workspace)
 
 template <int D, int NHB>
 struct PaShape {
-  static constexpr int STAGES = D == 64 ? 3 : (NHB == 1 ? 3 : 5);
-  static constexpr int PER_SM = NHB == 1 ? (D == 64 ? 3 : 2) : (D == 64 ? 2 : 1);
+  static constexpr int GROUPS = NHB == 1 ? (D == 64 ? 3 : 2) : (D == 64 ? 2 : 1);
+  static constexpr int STAGES = NHB == 1 ? 3 : (D == 64 ? 4 : 5);
+  static constexpr int CWARPS = 4 * GROUPS;                // consumer warps
+  static constexpr int THREADS = (CWARPS + GROUPS) * 32;
   static constexpr int HALF = PA_KT * 128;                 // bytes of 64 positions x 64 dims
   static constexpr int STAGE = 2 * (D / 64) * HALF;        // K then V
   static constexpr int QB = 8 * NHB * D * 2;
-  static constexpr int SMEM = STAGES * STAGE + 1024;
+  static constexpr int LD = D + 4;                         // floats of a part's row: values, max, sum
+  static constexpr int SMEM = GROUPS * STAGES * STAGE + 1024;
 };
 
 struct PagedAttnParams {
@@ -654,8 +660,8 @@ struct PagedAttnParams {
   int top, width, B, Hq, Hkv, G, n_pages, ps_log2, M, W;
   int dim_row, dim_head;      // tensor-map dimensions (1..3) of rows and heads; pages have the other
   float scale_log2;
-  float* part;                // [grid][2][G][D + 2]
-  int2* desc;                 // [grid]: (item, parts) of the cut item that this CTA begins
+  float* part;                // [grid][2][G][D + 4]: slot 1 the item that begins in the CTA
+  unsigned* arrived;          // [grid], zero between calls: parts of the cut item that CTA began
   DevStatus* status;
 };
 
@@ -691,39 +697,175 @@ __device__ __forceinline__ int pa_len(const PagedAttnParams& p, int b) {
 __device__ __forceinline__ unsigned long long low_bits(int n) {
   return n <= 0 ? 0ull : (n >= 64 ? ~0ull : (1ull << n) - 1);
 }
-
-struct PaMeta {
-  unsigned long long mask;   // visible positions of the tile
-  int item;                  // sequence * Hkv + kv head
-  int flags;                 // PA_FIRST, PA_LAST of the item's tiles in this CTA, PA_WHOLE, part slot
+// Shares of `total` tiles for n CTAs: the first total % n of them get one more.  (The host keeps
+// the number of tiles below 2^31.)
+struct PaShares {
+  int q, r;
+  __device__ PaShares(int total, int n) : q(total / n), r(total % n) {}
+  __device__ int begin(int c) const { return c * q + min(c, r); }
+  __device__ int owner(int x) const { return x < r * (q + 1) ? x / (q + 1) : r + (x - r * (q + 1)) / q; }
 };
-enum { PA_FIRST = 1, PA_LAST = 2, PA_WHOLE = 4, PA_SLOT1 = 8 };
+
+// what a stage's tile needs besides its bytes
+struct PaMeta {
+  unsigned long long mask;   // visible positions
+  int item;                  // sequence * Hkv + kv head
+  int last;                  // the item's last tile in this group; only then:
+  int cut;                   // the group has a part of the item only: 1 begun earlier, 2 begun here
+  int ends;                  // the item ends here
+  int c0, parts;             // the CTA that begins the item, and how many CTAs share it
+};
+// a group's part of a cut item, in shared memory
+struct PaPart {
+  int item;                  // -1: none
+  int c0, parts;
+};
+
+// (max, sum, 4 values) of a softmax over two sets of keys
+struct PaAcc {
+  float m, l, x[4];
+  __device__ void clear() {
+    m = -INFINITY;
+    l = x[0] = x[1] = x[2] = x[3] = 0.f;
+  }
+  __device__ void add(float m2, float l2, const float4& y) {
+    const float mn = fmaxf(m, m2), mu = mn == -INFINITY ? 0.f : mn;
+    const float wa = ex2_approx(m - mu), wb = ex2_approx(m2 - mu);
+    m = mn;
+    l = l * wa + l2 * wb;
+    x[0] = x[0] * wa + y.x * wb;
+    x[1] = x[1] * wa + y.y * wb;
+    x[2] = x[2] * wa + y.z * wb;
+    x[3] = x[3] * wa + y.w * wb;
+  }
+};
+__device__ __forceinline__ float pa_inverse(float l) {   // no key: zeros; a NaN stays one
+  return l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
+}
+__device__ __forceinline__ float pa_lse(float m, float l) {
+  return l == 0.f ? -INFINITY : 0.6931471805599453f * (m + log2f(l));
+}
+// 4 values of query head hh of an item, and its lse
+template <int D>
+__device__ __forceinline__ void pa_finish(const PagedAttnParams& p, int item, int hh, int quad, const PaAcc& a) {
+  const int b = item / p.Hkv, h = item % p.Hkv * p.G + hh;
+  const float inv = pa_inverse(a.l);
+  const long long at = b * p.out_stride + (long long)h * D + 4 * quad;
+  store_pair(p.out, p.out_dt, at, a.x[0] * inv, a.x[1] * inv);
+  store_pair(p.out, p.out_dt, at + 2, a.x[2] * inv, a.x[3] * inv);
+  if (p.lse != nullptr && quad == 0) p.lse[(long long)b * p.Hq + h] = pa_lse(a.m, a.l);
+}
+
+// Count a part of the item that CTA c0 began; true for the last of `parts`, which also returns
+// the counter to zero.  Releases what the caller's CTA wrote before (after a barrier), and
+// acquires what the others did.
+__device__ __forceinline__ bool pa_arrive(const PagedAttnParams& p, int c0, int parts) {
+  unsigned old;
+  asm volatile("atom.acq_rel.gpu.global.inc.u32 %0, [%1], %2;"
+               : "=r"(old) : "l"(p.arrived + c0), "r"((unsigned)(parts - 1)) : "memory");
+  return old == (unsigned)(parts - 1);
+}
+// After a wait that gave up, the counts are completed all the same, so that the next call on
+// the workspace finds them at zero: count this CTA's parts of cut items that it has not counted
+// (done: bit 0 an item begun earlier, bit 1 one that goes on), walking its share by items.
+__device__ __noinline__ void pa_arrive_rest(const PagedAttnParams& p, int b, int g, int t, int t0, int t1,
+                                            const PaShares& sh, int done) {
+  for (int cur = t0; cur < t1;) {
+    const int nt = pa_tiles(p, pa_len(p, b)).n_tiles;
+    const int beg = cur - t, end = beg + nt, stop = min(end, t1);
+    if ((beg < t0 || end > t1) && !(done & (beg < t0 ? 1 : 2))) {
+      const int c0 = sh.owner(beg);
+      pa_arrive(p, c0, sh.owner(end - 1) - c0 + 1);
+    }
+    cur = stop;
+    t = 0;
+    if (++g == p.Hkv) {
+      g = 0;
+      ++b;
+    }
+  }
+}
+
+// Merge the CTAs' parts of an item, by the CTA's consumer threads: D / 4 lanes (4 values each)
+// per part and head, SUBS such groups of lanes, dealt evenly to the heads and among a head's
+// parts in a fixed order, then a head's groups through sh (a row of LD floats each).  The loads
+// go past L1, which may hold an older line of a neighbouring part.
+template <int D, int CWARPS, typename Sync>
+__device__ __forceinline__ bool pa_join(const PagedAttnParams& p, int item, int c0, int parts, int tid, float* sh,
+                                        Sync& sync) {
+  constexpr int LPR = D / 4, SUBS = CWARPS * 32 / LPR, LD = D + 4;
+  const int sub = tid / LPR, quad = tid % LPR;
+  const int heads = min(p.G, SUBS), per_head = SUBS / heads;   // heads at a time
+  const int hs = sub / per_head, s0 = sub % per_head;
+  for (int h0 = 0; h0 < p.G; h0 += heads) {
+    PaAcc a;
+    a.clear();
+    if (hs < heads && h0 + hs < p.G) {
+      const float* src = p.part + (((long long)c0 * 2) * p.G + h0 + hs) * LD;
+#pragma unroll 8
+      for (int i = s0; i < parts; i += per_head) {
+        const float* row = src + ((long long)i * 2 + (i == 0 ? 1 : 0)) * p.G * LD;
+        const float2 ml = __ldcg(reinterpret_cast<const float2*>(row + D));
+        a.add(ml.x, ml.y, __ldcg(reinterpret_cast<const float4*>(row) + quad));
+      }
+    }
+    float* row = sh + sub * LD;
+    *reinterpret_cast<float4*>(row + 4 * quad) = make_float4(a.x[0], a.x[1], a.x[2], a.x[3]);
+    if (quad == 0) *reinterpret_cast<float2*>(row + D) = make_float2(a.m, a.l);
+    if (!sync()) return false;
+    if (sub < heads && h0 + sub < p.G) {
+      PaAcc t;
+      t.clear();
+      for (int k = 0; k < per_head; ++k) {
+        const float* r = sh + (sub * per_head + k) * LD;
+        t.add(r[D], r[D + 1], *reinterpret_cast<const float4*>(r + 4 * quad));
+      }
+      pa_finish<D>(p, item, h0 + sub, quad, t);
+    }
+    if (!sync()) return false;   // the rows are free again
+  }
+  return true;
+}
 
 template <typename E, int D, int NHB>
-__global__ void __launch_bounds__(PA_THREADS, PaShape<D, NHB>::PER_SM)
+__global__ void __launch_bounds__(PaShape<D, NHB>::THREADS, 1)
     paged_attn_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant__ CUtensorMap mapV,
                       const __grid_constant__ PagedAttnParams p) {
   using S = PaShape<D, NHB>;
-  constexpr int STAGES = S::STAGES;
+  constexpr int STAGES = S::STAGES, GROUPS = S::GROUPS, CWARPS = S::CWARPS, LD = S::LD;
   constexpr int NH = D / 64;
+  constexpr int NWARPS = S::THREADS / 32;
   extern __shared__ uint8_t pa_smem_raw[];
-  uint8_t* ring = align_smem<1024>(pa_smem_raw);
-  __shared__ uint64_t full[STAGES], empty[STAGES], merge_bar;
-  __shared__ __align__(16) PaMeta meta[STAGES];
-  __shared__ __align__(128) uint8_t qbuf[STAGES][S::QB];
-  __shared__ __align__(16) float mo[2][8][D + 4];   // pairwise merge of the warps (padded rows)
-  __shared__ float mm[2][8], ml[2][8];
-  __shared__ long long wsum[PA_THREADS / 32];
-  __shared__ long long start_at;                     // tile offset of the share inside sequence start_b
-  __shared__ int start_b, abort_flag;
+  uint8_t* rings = align_smem<1024>(pa_smem_raw);
+  __shared__ uint64_t full_bars[GROUPS][STAGES], empty_bars[GROUPS][STAGES], merge_bars[GROUPS], fin_bar;
+  __shared__ __align__(16) PaMeta metas[GROUPS][STAGES];
+  __shared__ __align__(128) uint8_t qbufs[GROUPS][2][S::QB];         // the queries of every other item
+  __shared__ __align__(16) float mos[GROUPS][2][8][LD];              // pairwise merge of a group's warps
+  // the groups' parts of cut items: one that ends in the group, one that goes on (the group's
+  // last item: with one block of heads it may stay in the merge rows)
+  __shared__ __align__(16) float prows[GROUPS][NHB][8 * NHB][LD];
+  auto part_row = [&](int k, int slot, int hh) -> float* {
+    if (NHB == 1 && slot == 1) return mos[k][0][hh];
+    return prows[k][slot][hh];
+  };
+  __shared__ PaPart pinfo[GROUPS][2];
+  __shared__ int wsum[NWARPS];
+  __shared__ int start[GROUPS][3];                   // the sequence, kv head and tile that a group starts at
+  __shared__ int counted, abort_flag;                // parts counted so far (bits as pa_arrive_rest)
+  __shared__ PaPart joins[2];                        // the cut items that this CTA joins
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
-    for (int i = 0; i < STAGES; ++i) {
-      mbar_init(&full[i], 1);
-      mbar_init(&empty[i], PA_CONSUMERS / 32);
+    for (int k = 0; k < GROUPS; ++k) {
+      for (int i = 0; i < STAGES; ++i) {
+        mbar_init(&full_bars[k][i], 1);
+        mbar_init(&empty_bars[k][i], 4);
+      }
+      mbar_init(&merge_bars[k], 4);
+      pinfo[k][0].item = pinfo[k][1].item = -1;
     }
-    mbar_init(&merge_bar, PA_CONSUMERS / 32);
-    abort_flag = 0;
+    mbar_init(&fin_bar, CWARPS);
+    joins[0].item = joins[1].item = -1;
+    abort_flag = counted = 0;
     fence_mbar_init();
     tma_prefetch_desc(&mapK);
     tma_prefetch_desc(&mapV);
@@ -731,69 +873,80 @@ __global__ void __launch_bounds__(PA_THREADS, PaShape<D, NHB>::PER_SM)
   pdl_wait();
   pdl_trigger();
 
-  // 1. this CTA's share of the tiles, and the sequence it starts in
-  const int per = (p.B + PA_THREADS - 1) / PA_THREADS;
+  // 1. the shares of this CTA and of its groups, and the sequences they start in
+  const int per = (p.B + S::THREADS - 1) / S::THREADS;
   const int b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
-  long long mine = 0;
+  int mine = 0;
   for (int i = b0; i < b1; ++i) {
     const int l = pa_len(p, i);
     const PaTiles t = pa_tiles(p, l);
     if (t.len != l && blockIdx.x == 0) report_error(p.status, DEV_ERR_BOUNDS, 601);
-    mine += t.n_tiles;
+    mine += t.n_tiles * p.Hkv;
   }
-  long long inc = mine;
+  int inc = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const long long up = __shfl_up_sync(0xffffffffu, inc, o);
+    const int up = __shfl_up_sync(0xffffffffu, inc, o);
     if (lane >= o) inc += up;
   }
   if (lane == 31) wsum[warp] = inc;
   __syncthreads();
-  long long before = inc - mine, total = 0;
-  for (int w = 0; w < PA_THREADS / 32; ++w) {
+  int before = inc - mine, total = 0;
+#pragma unroll
+  for (int w = 0; w < NWARPS; ++w) {
     if (w < warp) before += wsum[w];
     total += wsum[w];
   }
-  total *= p.Hkv;
-  const long long n_cta = min((long long)gridDim.x, total);
-  if (blockIdx.x >= n_cta) {
-    if (tid == 0) p.desc[blockIdx.x] = make_int2(0, 0);
-    return;
-  }
-  const long long t0 = blockIdx.x * total / n_cta, t1 = (blockIdx.x + 1) * total / n_cta;
-  if (t0 >= before * p.Hkv && t0 < (before + mine) * p.Hkv) {
-    long long left = t0 - before * p.Hkv;
-    int i = b0;
-    for (; i < b1; ++i) {
-      const long long c = (long long)pa_tiles(p, pa_len(p, i)).n_tiles * p.Hkv;
-      if (left < c) break;
-      left -= c;
+  const int n_cta = min((int)gridDim.x, total);
+  if ((int)blockIdx.x >= n_cta) return;
+  const PaShares shares(total, n_cta);
+  const int t0 = shares.begin(blockIdx.x), t1 = shares.begin(blockIdx.x + 1);
+  const int gq0 = (t1 - t0) / GROUPS, gr0 = (t1 - t0) % GROUPS;
+  auto share = [&](int k) { return t0 + k * gq0 + min(k, gr0); };   // of group k: share(k) .. share(k + 1)
+  if (mine > 0) {
+#pragma unroll
+    for (int k = 0; k < GROUPS; ++k) {
+      int left = share(k) - before;
+      if (left < 0 || left >= mine) continue;
+      for (int i = b0;; ++i) {
+        const int nt = pa_tiles(p, pa_len(p, i)).n_tiles;
+        if (left < nt * p.Hkv) {
+          start[k][0] = i;
+          start[k][1] = left / nt;
+          start[k][2] = left % nt;
+          break;
+        }
+        left -= nt * p.Hkv;
+      }
     }
-    start_b = i;
-    start_at = left;
   }
   __syncthreads();
-  const long long n_mine = t1 - t0;
+  const bool producer = warp >= CWARPS;
+  const int grp = producer ? warp - CWARPS : warp / 4;
+  const int u0 = share(grp), u1 = share(grp + 1), n_mine = u1 - u0;
+  uint64_t* full = full_bars[grp];
+  uint64_t* empty = empty_bars[grp];
+  uint8_t* ring = rings + grp * STAGES * S::STAGE;
 
-  if (warp == PA_CONSUMERS / 32) {
+  if (producer) {
     // ------------------------------ producer warp ------------------------------
+    if (n_mine == 0) return;
     const int ps = 1 << p.ps_log2;
     const int R = min(ps, PA_KT), n_chunk = PA_KT / R;    // a tile's page pieces
-    int b = start_b;
+    int b = start[grp][0], g = start[grp][1], t = start[grp][2];
     PaTiles sq = pa_tiles(p, pa_len(p, b));
-    int g = (int)(start_at / sq.n_tiles), t = (int)(start_at % sq.n_tiles);
     int next_len = b + 1 < p.B ? pa_len(p, b + 1) : 0;
-    int2 desc = make_int2(0, 0);
     bool ok = true;
-    // one tile's page piece of this lane: pool page (out of range where there is nothing to
-    // read), first row in the page, and the visible rows as bits
+    // One tile's page piece of this lane: the table's page (checked when it is used, so that the
+    // look-up of the next tile stays in flight meanwhile), the first row in it, and the visible
+    // rows as bits (0: nothing to read).
     struct Piece {
       int page, row;
       unsigned long long bits;
     };
     auto look = [&]() {
       Piece r;
-      r.page = p.n_pages;
+      r.page = -1;
       r.row = 0;
       r.bits = 0;
       if (lane < n_chunk) {
@@ -814,43 +967,26 @@ __global__ void __launch_bounds__(PA_THREADS, PaShape<D, NHB>::PER_SM)
         if (in && pos < sq.len) {
           r.bits = low_bits(min(R, sq.len - pos));
           if (p.W > 0) r.bits &= low_bits(p.M - pos) | ~low_bits((sq.len - pos) - p.W);
-          if (r.bits != 0) {
-            const int page = p.table[(long long)b * p.table_stride + logical];
-            if (page >= 0 && page < p.n_pages) {
-              r.page = page;
-            } else {
-              report_error(p.status, DEV_ERR_BOUNDS, 602);
-              r.bits = 0;
-            }
-          }
+          if (r.bits != 0) r.page = p.table[(long long)b * p.table_stride + logical];
         }
       }
       return r;
     };
     Piece cur = look();
-    int seg_first = 1;
-    long long i = 0;
+    bool first = true;
+    int q_tile[2] = {-STAGES, -STAGES};   // the tiles that came with the queries in the two buffers
+    int q_at = 0, stg = 0, i = 0;
+    uint32_t phase = 0;                   // of the current round through the ring
     for (; i < n_mine; ++i) {
-      const int stg = (int)(i % STAGES);
       // this tile's place in its item
-      const int item = b * p.Hkv + g;
-      const bool first = seg_first, last = i + 1 == n_mine || t + 1 == sq.n_tiles;
-      int flags = (first ? PA_FIRST : 0) | (last ? PA_LAST : 0);
-      if (first && t == 0) {
-        const long long end = t0 + i + sq.n_tiles;         // the item's end in the order of all tiles
-        if (end > t1) desc = make_int2(item, (int)((end * n_cta - 1) / total) - (int)blockIdx.x + 1);
-      }
-      // PA_WHOLE / PA_SLOT1 matter on the last tile: begun here at tile 0?
-      const long long seg_len_before = t;                  // tiles of the item before this one
-      const bool begun_here = seg_len_before <= i;         // its tile 0 is in this share
-      if (begun_here && t + 1 == sq.n_tiles) flags |= PA_WHOLE;
-      if (begun_here) flags |= PA_SLOT1;
-      const int cb = b, cg = g;
+      const int item = b * p.Hkv + g, cb = b, cg = g;
+      const bool q_due = first, last = i + 1 == n_mine || t + 1 == sq.n_tiles;
+      const int beg = u0 + i - t, end = beg + sq.n_tiles;   // the item's span in the order of all tiles
       // step to the next tile and start its look-up before waiting for a free stage
-      seg_first = 0;
+      first = false;
       if (++t == sq.n_tiles) {
         t = 0;
-        seg_first = 1;
+        first = true;
         if (++g == p.Hkv) {
           g = 0;
           ++b;
@@ -858,163 +994,217 @@ __global__ void __launch_bounds__(PA_THREADS, PaShape<D, NHB>::PER_SM)
           next_len = b + 1 < p.B ? pa_len(p, b + 1) : 0;
         }
       }
-      Piece nxt;
-      nxt.page = p.n_pages;
-      nxt.row = 0;
-      nxt.bits = 0;
+      Piece nxt = cur;
       if (i + 1 < n_mine) nxt = look();
-      if (i >= STAGES) {
-        ok = mbar_wait(&empty[stg], (uint32_t)(i / STAGES - 1) & 1u, &abort_flag, p.status, 603);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
+      if (i >= STAGES) ok = mbar_wait(&empty[stg], phase ^ 1u, &abort_flag, p.status, 603);
+      if (q_due) {   // the queries two items ago must have been taken: their tile released
+        const int back = i - q_tile[q_at];
+        if (ok && back < STAGES) {
+          const int qs = stg - back < 0 ? stg - back + STAGES : stg - back;
+          ok = mbar_wait(&empty[qs], stg - back < 0 ? phase ^ 1u : phase, &abort_flag, p.status, 608);
+        }
+        q_tile[q_at] = i;
+      }
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      int page = p.n_pages;                 // out of range: zeros
+      if (cur.bits != 0) {
+        if (cur.page >= 0 && cur.page < p.n_pages) {
+          page = cur.page;
+        } else {
+          report_error(p.status, DEV_ERR_BOUNDS, 602);
+          cur.bits = 0;
+        }
       }
       unsigned long long mask = cur.bits << (lane < n_chunk ? lane * R : 0);
       mask |= __shfl_xor_sync(0xffffffffu, mask, 1);
       mask |= __shfl_xor_sync(0xffffffffu, mask, 2);
       uint8_t* kt = ring + stg * S::STAGE;
       if (lane == 0) {
-        meta[stg].mask = mask;
-        meta[stg].item = item;
-        meta[stg].flags = flags;
-        const uint32_t q_bytes = first ? (uint32_t)(p.G * D * 2) : 0u;
+        PaMeta& mt = metas[grp][stg];
+        mt.mask = mask;
+        mt.last = last ? 1 : 0;
+        if (last) {
+          mt.item = item;
+          mt.cut = beg < u0 ? 1 : (end > u1 ? 2 : 0);
+          mt.ends = end <= u1 ? 1 : 0;
+          mt.c0 = beg < t0 ? shares.owner(beg) : (int)blockIdx.x;
+          mt.parts = (end > t1 ? shares.owner(end - 1) : (int)blockIdx.x) - mt.c0 + 1;
+        }
+        const uint32_t q_bytes = q_due ? (uint32_t)(p.G * D * 2) : 0u;
         mbar_arrive_expect_tx(&full[stg], S::STAGE + q_bytes);
-        if (first)
-          bulk_load(qbuf[stg], static_cast<const E*>(p.q) + cb * p.q_stride + (long long)cg * p.G * D, q_bytes,
+        if (q_due)
+          bulk_load(qbufs[grp][q_at], static_cast<const E*>(p.q) + cb * p.q_stride + (long long)cg * p.G * D, q_bytes,
                     &full[stg]);
       }
       __syncwarp();
       if (lane < n_chunk) {
-        auto coord = [&](int dim) { return p.dim_row == dim ? cur.row : (p.dim_head == dim ? cg : cur.page); };
-        const int c1 = coord(1), c2 = coord(2), c3 = coord(3);
+        auto coord = [&](int dim) { return p.dim_row == dim ? cur.row : (p.dim_head == dim ? cg : page); };
+        const int x1 = coord(1), x2 = coord(2), x3 = coord(3);
 #pragma unroll
         for (int h = 0; h < NH; ++h) {
-          tma_load_4d(kt + h * S::HALF + lane * R * 128, &mapK, &full[stg], h * 64, c1, c2, c3);
-          tma_load_4d(kt + (NH + h) * S::HALF + lane * R * 128, &mapV, &full[stg], h * 64, c1, c2, c3);
+          tma_load_4d(kt + h * S::HALF + lane * R * 128, &mapK, &full[stg], h * 64, x1, x2, x3);
+          tma_load_4d(kt + (NH + h) * S::HALF + lane * R * 128, &mapV, &full[stg], h * 64, x1, x2, x3);
         }
       }
+      if (q_due) q_at ^= 1;
       cur = nxt;
+      if (++stg == STAGES) {
+        stg = 0;
+        phase ^= 1u;
+      }
     }
+    // loads still in flight (all of them, if the consumers gave up) land before the CTA exits
     if (lane == 0) {
-      p.desc[blockIdx.x] = desc;
-      // loads still in flight (all of them, if the consumers gave up) land before the CTA exits
-      for (long long j = i > STAGES ? i - STAGES : 0; j < i; ++j)
-        mbar_wait(&full[j % STAGES], (uint32_t)(j / STAGES) & 1u, nullptr, p.status, 604);
+      for (int k = min(i, STAGES); k > 0; --k) {
+        if (--stg < 0) {
+          stg = STAGES - 1;
+          phase ^= 1u;
+        }
+        mbar_wait(&full[stg], phase, nullptr, p.status, 604);
+      }
     }
     return;
   }
 
   // ------------------------------ consumer warps ------------------------------
+  const int wg = warp & 3;                   // warp within the group
   const int gq = lane >> 2, tq = lane & 3;
   const uint32_t ring_u32 = smem_u32(ring);
-  const int k_row = warp * 16 + (lane & 7) + ((lane >> 4) & 1) * 8, k_chk = (lane >> 3) & 1;
-  const int v_row = warp * 16 + (lane & 7) + ((lane >> 3) & 1) * 8, v_chk = (lane >> 4) & 1;
-  uint32_t qa[D / 16][2 * NHB];
-  float m_run[NHB], l_run[NHB], o[NHB][D / 8][4];
-  uint32_t merge_phase = 0;
+  const int k_row = wg * 16 + (lane & 7) + ((lane >> 4) & 1) * 8, k_chk = (lane >> 3) & 1;
+  const int v_row = wg * 16 + (lane & 7) + ((lane >> 3) & 1) * 8, v_chk = (lane >> 4) & 1;
+  uint32_t merge_phase = 0, fin_phase = 0, phase = 0;
+  int stg = 0, i = 0;
   bool ok = true;
-  auto merge_sync = [&]() {   // the four consumer warps; bounded, so that a warp that gave up holds no one
+  // barriers of the group's and of all consumer warps; bounded, so that a warp that gave up
+  // holds no one for long
+  auto merge_sync = [&]() {
     __syncwarp();
-    if (lane == 0) mbar_arrive(&merge_bar);
-    const bool r = mbar_wait(&merge_bar, merge_phase & 1u, &abort_flag, p.status, 605);
+    if (lane == 0) mbar_arrive(&merge_bars[grp]);
+    const bool r = mbar_wait(&merge_bars[grp], merge_phase & 1u, &abort_flag, p.status, 605);
     ++merge_phase;
     return __all_sync(0xffffffffu, r) != 0;
   };
-  for (long long i = 0; i < n_mine && ok; ++i) {
-    const int stg = (int)(i % STAGES);
-    ok = mbar_wait(&full[stg], (uint32_t)(i / STAGES) & 1u, &abort_flag, p.status, 606);
-    ok = __all_sync(0xffffffffu, ok);
-    if (!ok) break;
-    const unsigned long long mask = meta[stg].mask;
-    const int item = meta[stg].item, flags = meta[stg].flags;
-    if (flags & PA_FIRST) {
-      const E* q = reinterpret_cast<const E*>(qbuf[stg]);
+  auto fin_sync = [&]() {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&fin_bar);
+    const bool r = mbar_wait(&fin_bar, fin_phase & 1u, &abort_flag, p.status, 607);
+    ++fin_phase;
+    return __all_sync(0xffffffffu, r) != 0;
+  };
+  for (int q_at = 0; i < n_mine && ok; q_at ^= 1) {   // one item's tiles in this group
+    uint32_t qa[D / 16][2 * NHB];
+    float m_run[NHB], l_run[NHB], o[NHB][D / 8][4];
 #pragma unroll
-      for (int hb = 0; hb < NHB; ++hb) {
-        m_run[hb] = -INFINITY;
-        l_run[hb] = 0.f;
+    for (int hb = 0; hb < NHB; ++hb) {
+      m_run[hb] = -INFINITY;
+      l_run[hb] = 0.f;
 #pragma unroll
-        for (int j = 0; j < D / 8; ++j) o[hb][j][0] = o[hb][j][1] = o[hb][j][2] = o[hb][j][3] = 0.f;
-        const bool row = hb * 8 + gq < p.G;
-        const E* qr = q + (hb * 8 + gq) * D + 2 * tq;
-#pragma unroll
-        for (int st = 0; st < D / 16; ++st) {
-          qa[st][2 * hb] = row ? *reinterpret_cast<const uint32_t*>(qr + st * 16) : 0u;
-          qa[st][2 * hb + 1] = row ? *reinterpret_cast<const uint32_t*>(qr + st * 16 + 8) : 0u;
-        }
-      }
+      for (int j = 0; j < D / 8; ++j) o[hb][j][0] = o[hb][j][1] = o[hb][j][2] = o[hb][j][3] = 0.f;
     }
-    const uint32_t m16 = (uint32_t)(mask >> (warp * 16)) & 0xffffu;
-    if (m16 != 0) {
-      const uint32_t kt = ring_u32 + stg * S::STAGE, vt = kt + NH * S::HALF;
-      float s0[4] = {0.f, 0.f, 0.f, 0.f}, s1[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int st = 0; st < D / 16; ++st) {
-        uint32_t f0, f1, f2, f3;
-        ldsm_x4(sw128_addr(kt + (st / 4) * S::HALF, k_row, 2 * (st & 3) + k_chk), f0, f1, f2, f3);
-        const uint32_t a1 = NHB == 2 ? qa[st][2 * NHB - 2] : 0u, a3 = NHB == 2 ? qa[st][2 * NHB - 1] : 0u;
-        Elem<E>::mma(s0, qa[st][0], a1, qa[st][1], a3, f0, f1);
-        Elem<E>::mma(s1, qa[st][0], a1, qa[st][1], a3, f2, f3);
-      }
-      // this lane's positions: 2tq, 2tq + 1, 2tq + 8, 2tq + 9 of the warp's 16
-      const uint32_t mb = m16 >> (2 * tq);
-      const bool vis[4] = {(mb & 1u) != 0, (mb & 2u) != 0, (mb & 0x100u) != 0, (mb & 0x200u) != 0};
-      uint32_t pa[NHB][4];
-#pragma unroll
-      for (int hb = 0; hb < NHB; ++hb) {
-        float v[4] = {s0[2 * hb] * p.scale_log2, s0[2 * hb + 1] * p.scale_log2, s1[2 * hb] * p.scale_log2,
-                      s1[2 * hb + 1] * p.scale_log2};
-        if (m16 != 0xffffu) {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) v[e] = vis[e] ? v[e] : -INFINITY;
-        }
-        float tm = fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3]));
-        tm = fmaxf(tm, __shfl_xor_sync(0xffffffffu, tm, 1));
-        tm = fmaxf(tm, __shfl_xor_sync(0xffffffffu, tm, 2));
-        const float m_new = fmaxf(m_run[hb], tm);
-        const float m_use = m_new == -INFINITY ? 0.f : m_new;   // every score so far is -inf
-        const float al = ex2_approx(m_run[hb] - m_use);
-        float e[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) e[k] = ex2_approx(v[k] - m_use);
-        m_run[hb] = m_new;
-        l_run[hb] = l_run[hb] * al + ((e[0] + e[1]) + (e[2] + e[3]));
-        if (__any_sync(0xffffffffu, al != 1.f)) {
-#pragma unroll
-          for (int j = 0; j < D / 8; ++j) {
-            o[hb][j][0] *= al; o[hb][j][1] *= al; o[hb][j][2] *= al; o[hb][j][3] *= al;
-          }
-        }
-        pa[hb][0] = Elem<E>::pack(e[0], e[1]);
-        pa[hb][2] = Elem<E>::pack(e[2], e[3]);
-        const float2 h0 = Elem<E>::unpack(pa[hb][0]), h2 = Elem<E>::unpack(pa[hb][2]);
-        pa[hb][1] = Elem<E>::pack(e[0] - h0.x, e[1] - h0.y);
-        pa[hb][3] = Elem<E>::pack(e[2] - h2.x, e[3] - h2.y);
-      }
-      // a hidden position's probability is 0, but its value may be anything (0 * NaN): its
-      // fragment halves are cleared
-      const uint32_t vm0 = (vis[0] ? 0xffffu : 0u) | (vis[1] ? 0xffff0000u : 0u);
-      const uint32_t vm1 = (vis[2] ? 0xffffu : 0u) | (vis[3] ? 0xffff0000u : 0u);
-#pragma unroll
-      for (int j = 0; j < D / 8; j += 2) {
-        uint32_t f0, f1, f2, f3;
-        ldsm_x4_t(sw128_addr(vt + (j / 8) * S::HALF, v_row, (j & 7) + v_chk), f0, f1, f2, f3);
-        if (m16 != 0xffffu) {
-          f0 &= vm0; f1 &= vm1; f2 &= vm0; f3 &= vm1;
-        }
+    PaMeta mt;
+    mt.item = mt.cut = mt.ends = mt.c0 = mt.parts = 0;
+    for (bool first = true, last = false; !last; first = false, ++i) {
+      ok = mbar_wait(&full[stg], phase, &abort_flag, p.status, 606);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      const unsigned long long mask = metas[grp][stg].mask;
+      last = metas[grp][stg].last != 0;
+      if (last) mt = metas[grp][stg];
+      if (first) {
+        const E* q = reinterpret_cast<const E*>(qbufs[grp][q_at]);
 #pragma unroll
         for (int hb = 0; hb < NHB; ++hb) {
-          Elem<E>::mma(o[hb][j], pa[hb][0], pa[hb][1], pa[hb][2], pa[hb][3], f0, f1);
-          Elem<E>::mma(o[hb][j + 1], pa[hb][0], pa[hb][1], pa[hb][2], pa[hb][3], f2, f3);
+          const bool row = hb * 8 + gq < p.G;
+          const E* qr = q + (hb * 8 + gq) * D + 2 * tq;
+#pragma unroll
+          for (int st = 0; st < D / 16; ++st) {
+            qa[st][2 * hb] = row ? *reinterpret_cast<const uint32_t*>(qr + st * 16) : 0u;
+            qa[st][2 * hb + 1] = row ? *reinterpret_cast<const uint32_t*>(qr + st * 16 + 8) : 0u;
+          }
         }
       }
+      const uint32_t m16 = (uint32_t)(mask >> (wg * 16)) & 0xffffu;
+      if (m16 != 0) {
+        const uint32_t kt = ring_u32 + stg * S::STAGE, vt = kt + NH * S::HALF;
+        float s0[4] = {0.f, 0.f, 0.f, 0.f}, s1[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int st = 0; st < D / 16; ++st) {
+          uint32_t f0, f1, f2, f3;
+          ldsm_x4(sw128_addr(kt + (st / 4) * S::HALF, k_row, 2 * (st & 3) + k_chk), f0, f1, f2, f3);
+          const uint32_t a1 = NHB == 2 ? qa[st][2 * NHB - 2] : 0u, a3 = NHB == 2 ? qa[st][2 * NHB - 1] : 0u;
+          Elem<E>::mma(s0, qa[st][0], a1, qa[st][1], a3, f0, f1);
+          Elem<E>::mma(s1, qa[st][0], a1, qa[st][1], a3, f2, f3);
+        }
+        // this lane's positions: 2tq, 2tq + 1, 2tq + 8, 2tq + 9 of the warp's 16
+        const uint32_t mb = m16 >> (2 * tq);
+        const bool vis[4] = {(mb & 1u) != 0, (mb & 2u) != 0, (mb & 0x100u) != 0, (mb & 0x200u) != 0};
+        uint32_t pa[NHB][4];
+#pragma unroll
+        for (int hb = 0; hb < NHB; ++hb) {
+          float v[4] = {s0[2 * hb] * p.scale_log2, s0[2 * hb + 1] * p.scale_log2, s1[2 * hb] * p.scale_log2,
+                        s1[2 * hb + 1] * p.scale_log2};
+          if (m16 != 0xffffu) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = vis[e] ? v[e] : -INFINITY;
+          }
+          float tm = fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3]));
+          tm = fmaxf(tm, __shfl_xor_sync(0xffffffffu, tm, 1));
+          tm = fmaxf(tm, __shfl_xor_sync(0xffffffffu, tm, 2));
+          const float m_new = fmaxf(m_run[hb], tm);
+          const float m_use = m_new == -INFINITY ? 0.f : m_new;   // every score so far is -inf
+          const float al = ex2_approx(m_run[hb] - m_use);
+          float e[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) e[k] = ex2_approx(v[k] - m_use);
+          m_run[hb] = m_new;
+          l_run[hb] = l_run[hb] * al + ((e[0] + e[1]) + (e[2] + e[3]));
+          if (__any_sync(0xffffffffu, al != 1.f)) {
+#pragma unroll
+            for (int j = 0; j < D / 8; ++j) {
+              o[hb][j][0] *= al; o[hb][j][1] *= al; o[hb][j][2] *= al; o[hb][j][3] *= al;
+            }
+          }
+          pa[hb][0] = Elem<E>::pack(e[0], e[1]);
+          pa[hb][2] = Elem<E>::pack(e[2], e[3]);
+          const float2 h0 = Elem<E>::unpack(pa[hb][0]), h2 = Elem<E>::unpack(pa[hb][2]);
+          pa[hb][1] = Elem<E>::pack(e[0] - h0.x, e[1] - h0.y);
+          pa[hb][3] = Elem<E>::pack(e[2] - h2.x, e[3] - h2.y);
+        }
+        // a hidden position's probability is 0, but its value may be anything (0 * NaN): its
+        // fragment halves are cleared
+        const uint32_t vm0 = (vis[0] ? 0xffffu : 0u) | (vis[1] ? 0xffff0000u : 0u);
+        const uint32_t vm1 = (vis[2] ? 0xffffu : 0u) | (vis[3] ? 0xffff0000u : 0u);
+#pragma unroll
+        for (int j = 0; j < D / 8; j += 2) {
+          uint32_t f0, f1, f2, f3;
+          ldsm_x4_t(sw128_addr(vt + (j / 8) * S::HALF, v_row, (j & 7) + v_chk), f0, f1, f2, f3);
+          if (m16 != 0xffffu) {
+            f0 &= vm0; f1 &= vm1; f2 &= vm0; f3 &= vm1;
+          }
+#pragma unroll
+          for (int hb = 0; hb < NHB; ++hb) {
+            Elem<E>::mma(o[hb][j], pa[hb][0], pa[hb][1], pa[hb][2], pa[hb][3], f0, f1);
+            Elem<E>::mma(o[hb][j + 1], pa[hb][0], pa[hb][1], pa[hb][2], pa[hb][3], f2, f3);
+          }
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&empty[stg]);   // this warp is done with the stage
+      if (++stg == STAGES) {
+        stg = 0;
+        phase ^= 1u;
+      }
     }
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&empty[stg]);   // this warp is done with the stage
-    if (!(flags & PA_LAST)) continue;
+    if (!ok) break;
 
-    // the item's tiles in this CTA are done: merge the four warps (2 and 3 into 0 and 1, then
-    // 1 into 0), warp 0 writes
-    const int b = item / p.Hkv, g = item % p.Hkv;
+    // the item's tiles in this group are done: merge the four warps (2 and 3 into 0 and 1,
+    // then 1 into 0), warp 0 writes the result or the part
+    const int b = mt.item / p.Hkv, g = mt.item % p.Hkv;
+    // the end of an item that began in an earlier CTA, all of it here in the first group: its
+    // part is final now and leaves at once, while the rest streams on
+    const bool early = grp == 0 && mt.cut == 1 && mt.c0 != (int)blockIdx.x && mt.ends;
+    float (*mo)[8][LD] = mos[grp];
 #pragma unroll
     for (int hb = 0; hb < NHB; ++hb) {
       float m = m_run[hb], l = l_run[hb];
@@ -1026,112 +1216,119 @@ __global__ void __launch_bounds__(PA_THREADS, PaShape<D, NHB>::PER_SM)
         acc[j][0] = o[hb][j][0] + o[hb][j][2];
         acc[j][1] = o[hb][j][1] + o[hb][j][3];
       }
-      auto put = [&](int slot) {
-        if (tq == 0) {
-          mm[slot][gq] = m;
-          ml[slot][gq] = l;
-        }
+      auto put = [&](float* row) {
+        if (tq == 0) *reinterpret_cast<float2*>(row + D) = make_float2(m, l);
 #pragma unroll
         for (int j = 0; j < D / 8; ++j)
-          *reinterpret_cast<float2*>(&mo[slot][gq][8 * j + 2 * tq]) = make_float2(acc[j][0], acc[j][1]);
+          *reinterpret_cast<float2*>(row + 8 * j + 2 * tq) = make_float2(acc[j][0], acc[j][1]);
       };
-      auto take = [&](int slot) {
-        const float m2 = mm[slot][gq], l2 = ml[slot][gq];
+      auto take = [&](const float* row) {
+        const float m2 = row[D], l2 = row[D + 1];
         const float mn = fmaxf(m, m2), mu = mn == -INFINITY ? 0.f : mn;
         const float wa = ex2_approx(m - mu), wb = ex2_approx(m2 - mu);
         m = mn;
         l = l * wa + l2 * wb;
 #pragma unroll
         for (int j = 0; j < D / 8; ++j) {
-          const float2 x = *reinterpret_cast<const float2*>(&mo[slot][gq][8 * j + 2 * tq]);
+          const float2 x = *reinterpret_cast<const float2*>(row + 8 * j + 2 * tq);
           acc[j][0] = acc[j][0] * wa + x.x * wb;
           acc[j][1] = acc[j][1] * wa + x.y * wb;
         }
       };
-      if (warp >= 2) put(warp - 2);
-      if (ok) ok = merge_sync();
-      if (!ok) break;
-      if (warp < 2) take(warp);
-      if (warp == 1) put(1);       // slot 1 was warp 1's own to read
+      if (wg >= 2) put(mo[wg - 2][gq]);
       ok = merge_sync();
       if (!ok) break;
-      if (warp == 0) take(1);
-      ok = merge_sync();           // the slots are free again
+      if (wg < 2) take(mo[wg][gq]);
+      if (wg == 1) put(mo[1][gq]);   // slot 1 was warp 1's own to read
+      ok = merge_sync();
       if (!ok) break;
-      const int hh = hb * 8 + gq;  // query head within the group
-      if (warp == 0 && hh < p.G) {
-        if (flags & PA_WHOLE) {
-          const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);   // no key: zeros; NaN stays
+      if (wg == 0) take(mo[1][gq]);
+      ok = merge_sync();             // the slots are free again
+      if (!ok) break;
+      const int hh = hb * 8 + gq;    // query head within the group
+      if (wg == 0 && hh < p.G) {
+        if (mt.cut == 0) {
+          const float inv = pa_inverse(l);
           const long long at = b * p.out_stride + (long long)(g * p.G + hh) * D + 2 * tq;
 #pragma unroll
           for (int j = 0; j < D / 8; ++j) store_pair(p.out, p.out_dt, at + 8 * j, acc[j][0] * inv, acc[j][1] * inv);
-          if (p.lse != nullptr && tq == 0)
-            p.lse[(long long)b * p.Hq + g * p.G + hh] = l == 0.f ? -INFINITY : 0.6931471805599453f * (m + log2f(l));
+          if (p.lse != nullptr && tq == 0) p.lse[(long long)b * p.Hq + g * p.G + hh] = pa_lse(m, l);
         } else {
-          float* dst = p.part + (((long long)blockIdx.x * 2 + ((flags & PA_SLOT1) ? 1 : 0)) * p.G + hh) * (D + 2);
-          if (tq == 0) *reinterpret_cast<float2*>(dst) = make_float2(m, l);
-#pragma unroll
-          for (int j = 0; j < D / 8; ++j)
-            *reinterpret_cast<float2*>(dst + 2 + 8 * j + 2 * tq) = make_float2(acc[j][0], acc[j][1]);
+          put(early ? p.part + ((long long)blockIdx.x * 2 * p.G + hh) * LD : part_row(grp, mt.cut - 1, hh));
+        }
+      }
+    }
+    if (ok && mt.cut != 0 && wg == 0) {
+      __syncwarp();
+      if (lane == 0) {
+        PaPart pi;
+        pi.item = mt.item;
+        pi.c0 = mt.c0;
+        pi.parts = mt.parts;
+        if (early) {
+          if (pa_arrive(p, mt.c0, mt.parts)) joins[0] = pi;   // joined when the CTA's groups are done
+          counted = 1;
+        } else {
+          pinfo[grp][mt.cut - 1] = pi;
         }
       }
     }
   }
-}
 
-// Join of an item that was cut: CTA x of the grid's first dimension stands for the attention
-// CTA that began the item, y for the query head.  The parts are its slot 1 and the slot 0 of
-// the CTAs after it; o = sum_i w_i o_i / sum_i w_i l_i, w_i = 2^(m_i - max m), added up by PJ
-// fixed interleaved groups of threads and then in group order, so the result does not depend
-// on scheduling.
-constexpr int PJ_THREADS = 256;
-template <int D>
-__global__ void __launch_bounds__(PJ_THREADS) paged_attn_join_kernel(const PagedAttnParams p) {
-  pdl_wait();
-  pdl_trigger();
-  constexpr int GROUPS = PJ_THREADS / D;
-  __shared__ float so[GROUPS][D], sl[GROUPS], sm[PJ_THREADS / 32];
-  const int2 desc = p.desc[blockIdx.x];
-  const int n = desc.y;
-  if (n == 0) return;
-  const int tid = threadIdx.x, hh = blockIdx.y;
-  const long long pstride = 2LL * p.G * (D + 2);
-  const float* first = p.part + (((long long)blockIdx.x * 2 + 1) * p.G + hh) * (D + 2);
-  const float* rest = p.part + ((long long)blockIdx.x * 2 * p.G + hh) * (D + 2);   // + i * pstride, i >= 1
-  auto src = [&](int i) { return i == 0 ? first : rest + i * pstride; };
-  float m = -INFINITY;
-  for (int i = tid; i < n; i += PJ_THREADS) m = fmaxf(m, src(i)[0]);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  if ((tid & 31) == 0) sm[tid >> 5] = m;
-  __syncthreads();
-  for (int w = 0; w < PJ_THREADS / 32; ++w) m = fmaxf(m, sm[w]);
-  const float mu = m == -INFINITY ? 0.f : m;
-  const int grp = tid / D, d = tid % D;
-  float O = 0.f, L = 0.f;
-#pragma unroll 8
-  for (int i = grp; i < n; i += GROUPS) {
-    const float* s = src(i);
-    const float w = ex2_approx(s[0] - mu);
-    L += w * s[1];
-    O += w * s[2 + d];
-  }
-  so[grp][d] = O;
-  if (d == 0) sl[grp] = L;
-  __syncthreads();
-  if (tid < D / 2) {
-    float a = 0.f, c = 0.f, l = 0.f;
-    for (int k = 0; k < GROUPS; ++k) {
-      a += so[k][2 * tid];
-      c += so[k][2 * tid + 1];
-      l += sl[k];
+  // ------------------------------ cut items ------------------------------
+  // The groups' parts in the order of the tiles; neighbours of one item are merged.  At most
+  // one item began in an earlier CTA (slot 0) and at most one goes on in a later one (slot 1).
+  if (ok) ok = fin_sync();
+  if (ok) {
+    constexpr int QUADS = D / 4;
+    bool far = false;
+    for (int f = 0; f < 2 * GROUPS;) {
+      const PaPart pi = pinfo[f >> 1][f & 1];
+      int e = f + 1;
+      if (pi.item >= 0) {
+        while (e < 2 * GROUPS && (pinfo[e >> 1][e & 1].item == pi.item || pinfo[e >> 1][e & 1].item < 0)) ++e;
+        for (int k = tid; k < p.G * QUADS; k += CWARPS * 32) {
+          const int hh = k / QUADS, quad = k % QUADS;
+          PaAcc a;
+          a.clear();
+          for (int x = f; x < e; ++x) {
+            if (pinfo[x >> 1][x & 1].item < 0) continue;
+            const float* row = part_row(x >> 1, x & 1, hh);
+            a.add(row[D], row[D + 1], *reinterpret_cast<const float4*>(row + 4 * quad));
+          }
+          if (pi.parts == 1) {
+            pa_finish<D>(p, pi.item, hh, quad, a);
+          } else {
+            float* dst = p.part + (((long long)blockIdx.x * 2 + (pi.c0 == (int)blockIdx.x ? 1 : 0)) * p.G + hh) * LD;
+            *reinterpret_cast<float4*>(dst + 4 * quad) = make_float4(a.x[0], a.x[1], a.x[2], a.x[3]);
+            if (quad == 0) *reinterpret_cast<float2*>(dst + D) = make_float2(a.m, a.l);
+          }
+        }
+        far = far || pi.parts > 1;
+      }
+      f = e;
     }
-    const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
-    const int b = desc.x / p.Hkv, h = desc.x % p.Hkv * p.G + hh;
-    store_pair(p.out, p.out_dt, b * p.out_stride + (long long)h * D + 2 * tid, a * inv, c * inv);
-    if (p.lse != nullptr && tid == 0)
-      p.lse[(long long)b * p.Hq + h] = l == 0.f ? -INFINITY : 0.6931471805599453f * (m + log2f(l));
+    if (far) {
+      ok = fin_sync();
+      if (ok && tid == 0) {
+        for (int f = 0; f < 2 * GROUPS; ++f) {
+          const PaPart pi = pinfo[f >> 1][f & 1];
+          const int slot = pi.c0 == (int)blockIdx.x ? 1 : 0;
+          if (pi.item >= 0 && pi.parts > 1 && !(counted & (1 << slot))) {   // (several groups' parts of one item)
+            if (pa_arrive(p, pi.c0, pi.parts)) joins[slot] = pi;
+            counted |= 1 << slot;
+          }
+        }
+      }
+      if (ok) ok = fin_sync();
+    }
+    // (every load of the rings has landed and been read: they are scratch now)
+    for (int s = 0; s < 2 && ok; ++s)
+      if (joins[s].item >= 0)
+        ok = pa_join<D, CWARPS>(p, joins[s].item, joins[s].c0, joins[s].parts, tid, reinterpret_cast<float*>(rings),
+                                fin_sync);
   }
+  if (!ok && tid == 0) pa_arrive_rest(p, start[0][0], start[0][1], start[0][2], t0, t1, shares, counted);
 }
 
 }  // namespace hymba

@@ -7,16 +7,16 @@ namespace {
 constexpr int PAGED_MAX_SELECT_WIDTH = 16384;   // one CTA ranks a sequence's pages in shared memory
 
 struct PagedWs {
-  size_t desc, part, keys, total;
+  size_t arrived, part, keys, total;
 };
-// The attention's parts and the selection's keys share the space after the status word: each
-// call uses it from its own first kernel on, and calls on one workspace follow one another.
+// The attention's part counters follow the status word (hymba_workspace_init zeroes both, and
+// every call leaves the counters at zero).  Its parts and the selection's keys share the rest:
+// calls on one workspace follow one another.
 PagedWs paged_layout(int head_dim, int n_kv_heads, int group, int batch, int max_pages) {
   PagedWs w;
-  w.desc = 256;
-  w.part = align256(w.desc + (size_t)PA_MAX_GRID * sizeof(int2));
-  w.keys = 256;
-  const size_t attn = w.part + (size_t)PA_MAX_GRID * 2 * group * (head_dim + 2) * 4;
+  w.arrived = 256;
+  w.part = w.keys = align256(w.arrived + (size_t)PA_MAX_GRID * sizeof(unsigned));
+  const size_t attn = w.part + (size_t)PA_MAX_GRID * 2 * group * (head_dim + 4) * 4;
   const size_t sel = w.keys + (size_t)batch * n_kv_heads * (size_t)max_pages * 8;
   w.total = align256(attn > sel ? attn : sel);
   return w;
@@ -119,7 +119,7 @@ int launch_paged_append(const hymba_paged_kv* kv, PagedAppendParams& p, float ro
   p.rotate = rope_base > 0.f ? 1 : 0;
   const int h2 = kv->head_dim / 2;
   for (int j = 0; p.rotate && j < h2; ++j)
-    p.turns[j] = std::pow((double)rope_base, -(double)j / h2) * 0.15915494309189535;
+    p.turns[j] = std::exp2(-std::log2((double)rope_base) * j / h2) * 0.15915494309189535;
   // the most runs there can be: a sequence of n tokens touches at most (n + 2 ps - 2) / ps
   // pages, and no more than it has tokens
   long long runs = p.B;
@@ -148,12 +148,9 @@ int launch_paged_attn_inst(const CUtensorMap& mk, const CUtensorMap& mv, const P
     HY_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM));
     attr[d & 63] = true;
   }
-  const int grid = std::min(sms * S::PER_SM, PA_MAX_GRID);
+  const int grid = std::min(sms, PA_MAX_GRID);
   prof_begin("paged_attn", st);
-  HY_CUDA(launch_pdl(kern, dim3(grid), dim3(PA_THREADS), S::SMEM, st, mk, mv, p));
-  prof_end(st);
-  prof_begin("paged_attn_join", st);
-  HY_CUDA(launch_pdl(paged_attn_join_kernel<D>, dim3(grid, p.G), dim3(PJ_THREADS), 0, st, p));
+  HY_CUDA(launch_pdl(kern, dim3(grid), dim3(S::THREADS), S::SMEM, st, mk, mv, p));
   prof_end(st);
   return HYMBA_OK;
 }
@@ -164,8 +161,12 @@ int launch_paged_attn(const hymba_paged_kv* kv, PagedAttnParams& p, uint8_t* ws,
   p.Hkv = kv->n_kv_heads;
   p.n_pages = kv->n_pages;
   p.ps_log2 = log2_int(kv->page_size);
-  p.desc = reinterpret_cast<int2*>(ws + L.desc);
+  p.arrived = reinterpret_cast<unsigned*>(ws + L.arrived);
   p.part = reinterpret_cast<float*>(ws + L.part);
+  // tiles are counted in 32 bits (2^31 of them are 16 TB of keys of one head)
+  const long long reach = p.page_idx != nullptr ? std::min(p.top, p.width) : p.width;
+  if ((double)p.B * p.Hkv * ((double)reach * kv->page_size / PA_KT + 2) >= 2147483648.0)
+    return fail(HYMBA_ERR_UNSUPPORTED, "%d sequences of %lld pages: too many keys for one call", p.B, reach);
   CUtensorMap mk, mv;
   const PagedDims o = paged_dims(kv);
   p.dim_row = o.at_row + 1;

@@ -255,17 +255,23 @@ class PagedCache:
     """
 
     def __init__(self, k, v, k_lo=None, k_hi=None):
-        _refuse_unless(k.dim() == 4 and k.shape == v.shape and k.dtype == v.dtype and k.stride() == v.stride(),
-                       "paged cache: k and v must be [n_pages, Hkv, page_size, D] of one type and layout")
-        _refuse_unless(k.stride(3) == 1, "paged cache: head_dim must be contiguous")
+        if not (k.dim() == 4 and k.shape == v.shape and k.dtype == v.dtype and k.stride() == v.stride()):
+            _refuse("paged cache: k and v must be [n_pages, Hkv, page_size, D] of one type and layout")
+        if k.stride(3) != 1:
+            _refuse("paged cache: head_dim must be contiguous")
         n, hkv, ps, D = k.shape
         for t in (k_lo, k_hi):
-            _refuse_unless(t is None or (tuple(t.shape) == (n, hkv, D) and t.dtype == k.dtype and t.is_contiguous()),
-                           "page bounds must be contiguous [n_pages, Hkv, D] in the pool's type")
-        _one_device(k, v, k_lo, k_hi)
+            if t is not None and not (t.shape == (n, hkv, D) and t.dtype == k.dtype and t.is_contiguous()):
+                _refuse("page bounds must be contiguous [n_pages, Hkv, D] in the pool's type")
         self.t = {"k": k, "v": v, "k_lo": k_lo, "k_hi": k_hi}
+        self.device = k.get_device()
+        self.dtype, self.n_kv_heads, self.head_dim = k.dtype, hkv, D
         self.c = PagedKV(_DT_CODE.get(k.dtype, -1), n, ps, hkv, D, k.stride(0), k.stride(1), k.stride(2), ptr(k),
                          ptr(v), ptr(k_lo), ptr(k_hi))
+        self.ref = ctypes.byref(self.c)
+        for t in (v, k_lo, k_hi):
+            if t is not None and t.get_device() != self.device or self.device < 0:
+                _refuse("paged cache: all tensors must be on one CUDA device")
 
     @classmethod
     def zeros(cls, n_pages, page_size, n_kv_heads, head_dim, dtype=torch.float16, bounds=False, device="cuda"):
@@ -274,43 +280,60 @@ class PagedCache:
         return cls(*kv, *[z(n_pages, n_kv_heads, head_dim) for _ in range(2 if bounds else 0)])
 
 
-def _refuse_unless(ok, msg):
-    if not ok:
-        raise HymbaError(ERR_INVALID_ARG, msg)
+# The paged calls run once per layer and token, so their checks are kept to plain comparisons
+# and a message is only put together when one fails.
+def _refuse(msg):
+    raise HymbaError(ERR_INVALID_ARG, msg)
 
 
-def _one_device(*tensors):
-    """The library launches on the current device: every tensor must live there."""
-    dev = {t.device for t in tensors if t is not None}
-    _refuse_unless(len(dev) == 1 and next(iter(dev)).type == "cuda", f"tensors must be on one CUDA device, got {dev}")
-    _refuse_unless(next(iter(dev)).index == torch.cuda.current_device(),
-                   f"tensors on {next(iter(dev))}, but the current device is cuda:{torch.cuda.current_device()}")
+def _paged_stream(cache, stream, *tensors):
+    """The stream to launch on, after checking that every tensor lives on the cache's device and
+    that this is the device the library will launch on."""
+    dev = cache.device
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            _refuse(f"a tensor on {t.device}, the paged cache on cuda:{dev}")
+    if stream is None:
+        stream = torch.cuda.current_stream(dev)
+    if stream.device_index != dev or torch.cuda.current_device() != dev:
+        _refuse(f"the paged cache is on cuda:{dev}, the current device or the stream is not")
+    return stream.cuda_stream
 
 
 def _page_table(table):
-    _refuse_unless(table.dim() == 2 and table.dtype == torch.int32 and table.stride(1) == 1,
-                   "block table must be int32 [batch, width] with contiguous rows")
+    st = table.stride()
+    if table.dim() != 2 or table.dtype != torch.int32 or st[1] != 1:
+        _refuse("block table must be int32 [batch, width] with contiguous rows")
+    B, width = table.shape
     # (a single row's stride is whatever torch made it)
-    stride = table.shape[1] if table.shape[0] == 1 else table.stride(0)
-    return PageTable(ptr(table), table.shape[0], table.shape[1], stride)
+    return PageTable(table.data_ptr(), B, width, width if B == 1 else st[0]), B
 
 
 def _int32_vector(t, n, name):
-    _refuse_unless(t.dtype == torch.int32 and t.dim() == 1 and t.shape[0] == n and t.is_contiguous(),
-                   f"{name} must be a contiguous int32 vector of {n}")
+    if t.dtype != torch.int32 or t.shape != (n,) or not t.is_contiguous():
+        _refuse(f"{name} must be a contiguous int32 vector of {n}")
+    return t.data_ptr()
 
 
 def _head_rows(t, D, name):
     """Row stride of [rows, heads, D] whose heads are contiguous."""
-    _refuse_unless(t.dim() == 3 and t.shape[2] == D and t.stride(2) == 1 and (t.shape[1] == 1 or t.stride(1) == D),
-                   f"{name} must be [rows, heads, {D}] with contiguous heads")
-    return t.shape[1] * D if t.shape[0] <= 1 else t.stride(0)
+    sh, st = t.shape, t.stride()
+    if len(sh) != 3 or sh[2] != D or st[2] != 1 or (st[1] != D and sh[1] != 1):
+        _refuse(f"{name} must be [rows, heads, {D}] with contiguous heads")
+    return sh[1] * D if sh[0] <= 1 else st[0]
+
+
+def _page_list(page_idx, cache, B):
+    if not (page_idx.dtype == torch.int32 and page_idx.dim() == 3 and page_idx.is_contiguous() and
+            page_idx.shape[:2] == (B, cache.n_kv_heads)):
+        _refuse("page_idx must be contiguous int32 [batch, Hkv, top_pages]")
+    return page_idx.data_ptr(), page_idx.shape[2]
 
 
 def paged_workspace_size(cache: PagedCache, batch, n_q_heads, max_pages) -> int:
     """Workspace bytes for paged_select and paged_attention (max_pages: the block table's width)."""
     n = ctypes.c_size_t()
-    check(lib().hymba_paged_workspace_size(ctypes.byref(cache.c), batch, n_q_heads, max_pages, ctypes.byref(n)))
+    check(lib().hymba_paged_workspace_size(cache.ref, batch, n_q_heads, max_pages, ctypes.byref(n)))
     return n.value
 
 
@@ -321,52 +344,49 @@ def paged_append(cache: PagedCache, table, start, k, v, ws, q=None, q_out=None, 
 
     table [B, width], start [B] int32; cu_new [B + 1] int32 gives each sequence's rows (None: one
     token per sequence).  k and v may be None together.  rope_base 0: no rotation."""
-    D, Hkv = cache.c.head_dim, cache.c.n_kv_heads
+    if (k is None) != (v is None) or (q is None) != (q_out is None) or (k is None and q is None):
+        _refuse("paged_append: k and v go together, q and q_out go together")
+    st = _paged_stream(cache, stream, table, start, k, v, ws, q, q_out, cu_new)
+    tb, B = _page_table(table)
+    D = cache.head_dim
     src = k if k is not None else q
-    _refuse_unless(src is not None and (k is None) == (v is None) and (q is None) == (q_out is None),
-                   "paged_append: k and v go together, q and q_out go together")
-    _one_device(cache.t["k"], table, start, k, v, ws, q, q_out, cu_new)
-    tb = _page_table(table)
-    _int32_vector(start, tb.batch, "start")
-    if cu_new is not None:
-        _int32_vector(cu_new, tb.batch + 1, "cu_new")
-    T = src.shape[0]
-    strides = [0, 0, 0]
-    for i, (t, heads, name) in enumerate(((k, Hkv, "k"), (v, Hkv, "v"), (q, None, "q"))):
-        if t is not None:
-            strides[i] = _head_rows(t, D, name)
-            _refuse_unless(t.shape[0] == T and t.dtype == src.dtype and (heads is None or t.shape[1] == heads),
-                           f"paged_append: {name} {tuple(t.shape)} {t.dtype}")
-    Hq = q.shape[1] if q is not None else 0
-    if q_out is not None:
-        _refuse_unless(q_out.shape == q.shape and q_out.dtype == cache.t["k"].dtype and q_out.is_contiguous(),
-                       "paged_append: q_out must be contiguous, shaped like q, in the pool's type")
-    check(lib().hymba_paged_append(ctypes.byref(cache.c), ctypes.byref(tb), ptr(start), ptr(cu_new), T,
-                                   _DT_CODE.get(src.dtype, -1), ptr(k), strides[0], ptr(v), strides[1], ptr(q),
-                                   strides[2], Hq, ptr(q_out), rope_base, ptr(ws), ws.numel(),
-                                   stream_handle(stream)))
-
-
-def _query_rows(cache, q, batch):
-    _refuse_unless(q.dim() == 3 and q.shape[0] == batch and q.dtype == cache.t["k"].dtype,
-                   "q must be [batch, Hq, D] in the pool's type")
-    return _head_rows(q, cache.c.head_dim, "q")
+    dt, T = src.dtype, src.shape[0]
+    kp = vp = qp = qo = None
+    ks = vs = qs = Hq = 0
+    if k is not None:
+        want = (T, cache.n_kv_heads, D)
+        if k.shape != want or v.shape != want or v.dtype != dt:
+            _refuse(f"paged_append: k {tuple(k.shape)} {k.dtype}, v {tuple(v.shape)} {v.dtype}")
+        kp, vp, ks, vs = k.data_ptr(), v.data_ptr(), _head_rows(k, D, "k"), _head_rows(v, D, "v")
+    if q is not None:
+        qs, Hq = _head_rows(q, D, "q"), q.shape[1]
+        if q.shape[0] != T or q.dtype != dt:
+            _refuse(f"paged_append: q {tuple(q.shape)} {q.dtype}")
+        if q_out.shape != q.shape or q_out.dtype != cache.dtype or not q_out.is_contiguous():
+            _refuse("paged_append: q_out must be contiguous, shaped like q, in the pool's type")
+        qp, qo = q.data_ptr(), q_out.data_ptr()
+    rc = lib().hymba_paged_append(cache.ref, ctypes.byref(tb), _int32_vector(start, B, "start"),
+                                  None if cu_new is None else _int32_vector(cu_new, B + 1, "cu_new"), T,
+                                  _DT_CODE.get(dt, -1), kp, ks, vp, vs, qp, qs, Hq, qo, rope_base, ws.data_ptr(),
+                                  ws.numel(), st)
+    if rc:
+        check(rc)
 
 
 def paged_select(cache: PagedCache, q, table, seq_lens, page_idx, ws, n_first=1, n_last=1, stream=None):
     """hymba_paged_select: page_idx [B, Hkv, top] int32 receives, per sequence and KV head, the
     pages (numbers within the sequence, ascending, -1 behind the last) that the rotated query
     q [B, Hq, D] should read: the first n_first, the last n_last and the best by page bounds."""
-    _one_device(cache.t["k"], q, table, seq_lens, page_idx, ws)
-    tb = _page_table(table)
-    _int32_vector(seq_lens, tb.batch, "seq_lens")
-    qs = _query_rows(cache, q, tb.batch)
-    _refuse_unless(page_idx.dtype == torch.int32 and page_idx.dim() == 3 and page_idx.is_contiguous() and
-                   tuple(page_idx.shape[:2]) == (tb.batch, cache.c.n_kv_heads),
-                   "page_idx must be contiguous int32 [batch, Hkv, top_pages]")
-    check(lib().hymba_paged_select(ctypes.byref(cache.c), ctypes.byref(tb), ptr(seq_lens), ptr(q), qs, q.shape[1],
-                                   n_first, n_last, page_idx.shape[2], ptr(page_idx), ptr(ws), ws.numel(),
-                                   stream_handle(stream)))
+    st = _paged_stream(cache, stream, q, table, seq_lens, page_idx, ws)
+    tb, B = _page_table(table)
+    qs = _head_rows(q, cache.head_dim, "q")
+    if q.shape[0] != B or q.dtype != cache.dtype:
+        _refuse("q must be [batch, Hq, D] in the pool's type")
+    idx, top = _page_list(page_idx, cache, B)
+    rc = lib().hymba_paged_select(cache.ref, ctypes.byref(tb), _int32_vector(seq_lens, B, "seq_lens"), q.data_ptr(),
+                                  qs, q.shape[1], n_first, n_last, top, idx, ws.data_ptr(), ws.numel(), st)
+    if rc:
+        check(rc)
 
 
 def paged_attention(cache: PagedCache, q, table, seq_lens, out, ws, scale=None, n_meta=0, window=0, page_idx=None,
@@ -374,25 +394,22 @@ def paged_attention(cache: PagedCache, q, table, seq_lens, out, ws, scale=None, 
     """hymba_paged_attention: out [B, Hq, D] = attention of one (rotated) query per sequence over
     the first seq_lens[b] positions of its pages; with window > 0 over the first n_meta positions
     and the last `window`; with page_idx over the listed pages.  scale: 1/sqrt(D) by default."""
-    _one_device(cache.t["k"], q, table, seq_lens, out, ws, page_idx, lse)
-    tb = _page_table(table)
-    _int32_vector(seq_lens, tb.batch, "seq_lens")
-    qs = _query_rows(cache, q, tb.batch)
-    _refuse_unless(out.shape == q.shape, "out must be shaped like q")
-    top = 0
-    if page_idx is not None:
-        _refuse_unless(page_idx.dtype == torch.int32 and page_idx.dim() == 3 and page_idx.is_contiguous() and
-                       tuple(page_idx.shape[:2]) == (tb.batch, cache.c.n_kv_heads),
-                       "page_idx must be contiguous int32 [batch, Hkv, top_pages]")
-        top = page_idx.shape[2]
-    if lse is not None:
-        _refuse_unless(lse.dtype == torch.float32 and tuple(lse.shape) == (tb.batch, q.shape[1]) and
-                       lse.is_contiguous(), "lse must be contiguous fp32 [batch, Hq]")
-    scale = cache.c.head_dim ** -0.5 if scale is None else scale
-    check(lib().hymba_paged_attention(ctypes.byref(cache.c), ctypes.byref(tb), ptr(seq_lens), ptr(q), qs, q.shape[1],
-                                      scale, n_meta, window, ptr(page_idx), top, ptr(out), _DT_CODE.get(out.dtype, -1),
-                                      _head_rows(out, cache.c.head_dim, "out"), ptr(lse), ptr(ws), ws.numel(),
-                                      stream_handle(stream)))
+    st = _paged_stream(cache, stream, q, table, seq_lens, out, ws, page_idx, lse)
+    tb, B = _page_table(table)
+    D = cache.head_dim
+    qs, os = _head_rows(q, D, "q"), _head_rows(out, D, "out")
+    Hq = q.shape[1]
+    if q.shape[0] != B or q.dtype != cache.dtype or out.shape != q.shape:
+        _refuse("q must be [batch, Hq, D] in the pool's type, and out shaped like it")
+    idx, top = (None, 0) if page_idx is None else _page_list(page_idx, cache, B)
+    if lse is not None and (lse.dtype != torch.float32 or lse.shape != (B, Hq) or not lse.is_contiguous()):
+        _refuse("lse must be contiguous fp32 [batch, Hq]")
+    rc = lib().hymba_paged_attention(cache.ref, ctypes.byref(tb), _int32_vector(seq_lens, B, "seq_lens"),
+                                     q.data_ptr(), qs, Hq, D ** -0.5 if scale is None else scale, n_meta, window, idx,
+                                     top, out.data_ptr(), _DT_CODE.get(out.dtype, -1), os,
+                                     None if lse is None else lse.data_ptr(), ws.data_ptr(), ws.numel(), st)
+    if rc:
+        check(rc)
 
 
 def workspace_size(dims, batch, n_tokens, x_has_meta=0, mode=MODE_PREFILL):
