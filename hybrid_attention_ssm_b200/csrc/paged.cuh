@@ -6,6 +6,8 @@
 // of sequence b is row p % page_size of page table[b][p / page_size].  Optional page bounds
 // keep the smallest and largest key value per channel, [page, kv head, D].
 #pragma once
+#include <type_traits>
+
 #include "common.cuh"
 #include "misc.cuh"
 
@@ -21,6 +23,15 @@ struct Elem<__half> {
   static constexpr bool IS_F16 = true;
   __device__ static uint32_t pack(float lo, float hi) { return pack_f16x2(lo, hi); }
   __device__ static float2 unpack(uint32_t v) { return __half22float2(*reinterpret_cast<__half2*>(&v)); }
+  __device__ static uint32_t min2(uint32_t a, uint32_t b) {
+    const __half2 r = __hmin2(*reinterpret_cast<__half2*>(&a), *reinterpret_cast<__half2*>(&b));
+    return *reinterpret_cast<const uint32_t*>(&r);
+  }
+  __device__ static uint32_t max2(uint32_t a, uint32_t b) {
+    const __half2 r = __hmax2(*reinterpret_cast<__half2*>(&a), *reinterpret_cast<__half2*>(&b));
+    return *reinterpret_cast<const uint32_t*>(&r);
+  }
+  static constexpr uint32_t INF2 = 0x7c007c00u;
   // d (16x8 fp32) += a (16x16, row-major) * b (16x8, column-major)
   __device__ static void mma(float* d, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
     mma_16816(d, a0, a1, a2, a3, b0, b1);
@@ -31,6 +42,15 @@ struct Elem<__nv_bfloat16> {
   static constexpr bool IS_F16 = false;
   __device__ static uint32_t pack(float lo, float hi) { return pack_bf16x2(lo, hi); }
   __device__ static float2 unpack(uint32_t v) { return __bfloat1622float2(*reinterpret_cast<__nv_bfloat162*>(&v)); }
+  __device__ static uint32_t min2(uint32_t a, uint32_t b) {
+    const __nv_bfloat162 r = __hmin2(*reinterpret_cast<__nv_bfloat162*>(&a), *reinterpret_cast<__nv_bfloat162*>(&b));
+    return *reinterpret_cast<const uint32_t*>(&r);
+  }
+  __device__ static uint32_t max2(uint32_t a, uint32_t b) {
+    const __nv_bfloat162 r = __hmax2(*reinterpret_cast<__nv_bfloat162*>(&a), *reinterpret_cast<__nv_bfloat162*>(&b));
+    return *reinterpret_cast<const uint32_t*>(&r);
+  }
+  static constexpr uint32_t INF2 = 0x7f807f80u;
   __device__ static void mma(float* d, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
     asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
                  "{%0, %1, %2, %3};"
@@ -61,15 +81,29 @@ __device__ __forceinline__ void store_pair(void* out, int dt, long long i, float
 // p * theta_j (theta_j = base^(-2j/D), the pair (j, j + D/2)), and the rotated key and the
 // value, rounded once to the pool's type, go to row p % page_size of the sequence's page.
 //
-// CTA = (run, kv head): a run is the tokens of one sequence that fall into one page, so one
-// CTA alone owns a page's rows and bounds of its head (no atomics, and the bounds need no
-// second pass).  The CTA also rotates the G query heads of its group, which share the angles:
-// RC rows' cosines and sines are computed once into shared memory (the angle in turns is
-// reduced in double precision, so far positions keep their phase) and used by G + 1 heads.
-// Threads 0..127 take the chunk's keys (4 pairs each), threads 128..255 its values, then
-// all of them the queries.
+// A thread owns some pairs of a token: it computes their angles once and applies them to the
+// key and to the query heads of its kv head; the value is copied.  Angles are phases in units
+// of 2^-64 turns, pos * turn_j modulo 2^64 in integers, so far positions keep theirs.
+//
+// One token per sequence (paged_append_step_kernel): thread = (sequence, kv head, 4 pairs), and
+// each page's bounds are widened by the thread that owns the channels.
+//
+// Several (paged_append_kernel): persistent CTAs, three per SM, take the items (run, kv head) in
+// turn, a run being the tokens of one sequence that fall into one page: one CTA alone owns a
+// page's rows and bounds of a head, so there are no atomics and no second pass, and the heads
+// of a run, whose rows are neighbours in memory, are under way at the same time (equal
+// contiguous shares instead: 61 -> 57 us at 4 x 8320 tokens).  A producer warp streams the items' rows through a ring by TMA, 8 tokens to a box, so
+// the bytes in flight cost neither registers nor instructions; eight consumer warps take a
+// stage's rows, 4 pairs of a row per thread.
 // ----------------------------------------------------------------------------------------
-constexpr int PAP_THREADS = 256;
+constexpr int PAP_STEP_THREADS = 64;
+constexpr int PAP_CONSUMERS = 256;
+constexpr int PAP_THREADS = PAP_CONSUMERS + 32;
+constexpr int PAP_PER_SM = 3;
+constexpr int PAP_BOX = 8;                 // tokens per TMA box
+constexpr int PAP_STAGES = 2;
+constexpr int PAP_STAGE_BYTES = 32768;     // (one box of the widest group needs more)
+constexpr int PAP_SMEM_MAX = PAP_STAGES * PAP_BOX * (16 + 2) * 128 * 4;
 
 struct PagedAppendParams {
   const void *q, *k, *v;            // [T] rows of Hq*D, Hkv*D, Hkv*D elements; q may be NULL
@@ -84,40 +118,240 @@ struct PagedAppendParams {
   const int* table;
   long long table_stride;
   int width, B, T, G, Hkv, n_pages, ps_log2, rotate;
+  int chunk;                        // several tokens: rows of a stage
   void *pk, *pv;                    // the pool; pk NULL: only the queries are rotated
   long long page_stride, head_stride, row_stride;
   void *k_lo, *k_hi;                // [n_pages, Hkv, D], or NULL
   DevStatus* status;
-  double turns[64];                 // theta_j / (2 pi)
+  unsigned long long turns[64];     // theta_j / (2 pi) in units of 2^-64
 };
 
-// 4 consecutive source elements as floats
-__device__ __forceinline__ void pap_load4(const PagedAppendParams& p, const void* base, long long i, float* f) {
-  if (p.src == PDT_F32) {
-    const float* s = static_cast<const float*>(base) + i;
-    float4 a = *reinterpret_cast<const float4*>(s);
-    for (int n = 1; n < p.n_slices; ++n) {
-      const float4 c = *reinterpret_cast<const float4*>(s + n * p.slice_stride);
-      a.x += c.x; a.y += c.y; a.z += c.z; a.w += c.w;
-    }
-    f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
-  } else {
-    const uint2 r = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(base) + i);
-    float2 a, b;
-    if (p.src == PDT_F16) {
-      a = Elem<__half>::unpack(r.x);
-      b = Elem<__half>::unpack(r.y);
-    } else {
-      a = Elem<__nv_bfloat16>::unpack(r.x);
-      b = Elem<__nv_bfloat16>::unpack(r.y);
-    }
-    f[0] = a.x; f[1] = a.y; f[2] = b.x; f[3] = b.y;
+// 4 consecutive source elements, as they are loaded; as two packed fp32 pairs, and rounded
+template <int SRC>
+struct PapRaw {
+  using T = typename std::conditional<SRC == PDT_F16, __half, __nv_bfloat16>::type;
+  uint2 r;
+  __device__ void load(const PagedAppendParams&, const void* base, long long i) {
+    r = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(base) + i);
   }
+  __device__ void get(uint64_t* f) const {
+    const float2 a = Elem<T>::unpack(r.x), b = Elem<T>::unpack(r.y);
+    f[0] = f2_pack(a.x, a.y);
+    f[1] = f2_pack(b.x, b.y);
+  }
+};
+template <>
+struct PapRaw<PDT_F32> {
+  using T = float;
+  float4 r;
+  __device__ void load(const PagedAppendParams& p, const void* base, long long i) {
+    const float* s = static_cast<const float*>(base) + i;
+    r = *reinterpret_cast<const float4*>(s);
+    for (int n = 1; n < p.n_slices; ++n) {   // split-K slices, in order
+      const float4 c = *reinterpret_cast<const float4*>(s + n * p.slice_stride);
+      r.x += c.x; r.y += c.y; r.z += c.z; r.w += c.w;
+    }
+  }
+  __device__ void get(uint64_t* f) const {
+    f[0] = f2_pack(r.x, r.y);
+    f[1] = f2_pack(r.z, r.w);
+  }
+};
+template <typename E>
+__device__ __forceinline__ uint2 pap_round(const uint64_t* f) {
+  return make_uint2(Elem<E>::pack(f2_lo(f[0]), f2_hi(f[0])), Elem<E>::pack(f2_lo(f[1]), f2_hi(f[1])));
 }
 
+// cos and sin of pairs j0 .. j0 + N - 1 at a position, as packed fp32 pairs.  The phase's
+// nearest quarter turn is split off in integers; the rest, at most 1/8 turn, goes into the
+// Taylor polynomials of sin(2 pi r) and cos(2 pi r) (remainders below 2e-9 and 2e-10).
+template <int N>
+struct PapTurn {
+  uint64_t cs[N / 2], sn[N / 2], neg[N / 2];   // neg = -sn
+  __device__ __forceinline__ void at(const PagedAppendParams& p, int pos, int j0) {
+#pragma unroll
+    for (int e = 0; e < N / 2; ++e) {
+      uint32_t quarter[2];
+      float r[2];
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const uint32_t ph = (uint32_t)(((unsigned long long)(uint32_t)pos * p.turns[j0 + 2 * e + k]) >> 32);
+        quarter[k] = (ph + 0x20000000u) >> 30;
+        r[k] = (float)(int)(ph - (quarter[k] << 30)) * 0x1p-32f;
+      }
+      const uint64_t x = f2_pack(r[0], r[1]), x2 = f2_mul(x, x);
+      auto c2 = [](float v) { return f2_pack(v, v); };
+      uint64_t s = f2_fma(x2, c2(42.058693944897655f), c2(-76.70585975306136f));
+      s = f2_fma(s, x2, c2(81.60524927607504f));
+      s = f2_fma(s, x2, c2(-41.34170224039976f));
+      s = f2_mul(f2_fma(s, x2, c2(6.283185307179586f)), x);
+      uint64_t c = f2_fma(x2, c2(-26.426256783374388f), c2(60.244641371876656f));
+      c = f2_fma(c, x2, c2(-85.45681720669373f));
+      c = f2_fma(c, x2, c2(64.93939402266829f));
+      c = f2_fma(c, x2, c2(-19.739208802178716f));
+      c = f2_fma(c, x2, c2(1.f));
+      float sv[2] = {f2_lo(s), f2_hi(s)}, cv[2] = {f2_lo(c), f2_hi(c)};
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {   // sin and cos of r + quarter / 4
+        const float a = (quarter[k] & 1u) ? cv[k] : sv[k], b = (quarter[k] & 1u) ? sv[k] : cv[k];
+        sv[k] = __uint_as_float(__float_as_uint(a) ^ ((quarter[k] & 2u) << 30));
+        cv[k] = __uint_as_float(__float_as_uint(b) ^ (((quarter[k] + 1u) & 2u) << 30));
+      }
+      cs[e] = f2_pack(cv[0], cv[1]);
+      sn[e] = f2_pack(sv[0], sv[1]);
+      neg[e] = f2_pack(-sv[0], -sv[1]);
+    }
+  }
+  // (a, b) of pair 2e and 2e + 1 turned
+  __device__ __forceinline__ void apply(int e, uint64_t& a, uint64_t& b) const {
+    const uint64_t x = f2_fma(b, neg[e], f2_mul(a, cs[e]));
+    b = f2_fma(a, sn[e], f2_mul(b, cs[e]));
+    a = x;
+  }
+};
+
+// One token and kv head of a thread: the key and value into the pool's row (element offset,
+// head included; -1: no place), the group's query heads into q_out.  k returns the stored key
+// (low and high channels), big the largest magnitudes rounded so far.
+template <typename E, int D, int SRC>
+__device__ __forceinline__ void pap_token(const PagedAppendParams& p, const PapTurn<4>& turn, long long tok,
+                                          long long row, int g, int part, uint2* k, uint32_t& big) {
+  constexpr int H2 = D / 2, QB = 4;   // query heads whose loads are in flight together
+  PapRaw<SRC> kr[2], vr[2], qr[QB][2];
+  if (row >= 0) {
+    const long long ka = tok * p.k_stride + g * D + part * 4, va = tok * p.v_stride + g * D + part * 4;
+    kr[0].load(p, p.k, ka);
+    kr[1].load(p, p.k, ka + H2);
+    vr[0].load(p, p.v, va);
+    vr[1].load(p, p.v, va + H2);
+  }
+  const long long qa = tok * p.q_stride + g * p.G * D + part * 4;
+  auto load_q = [&](int h0) {
+#pragma unroll
+    for (int h = 0; h < QB; ++h) {
+      if (h0 + h < p.G) {
+        qr[h][0].load(p, p.q, qa + (h0 + h) * D);
+        qr[h][1].load(p, p.q, qa + (h0 + h) * D + H2);
+      }
+    }
+  };
+  if (p.q != nullptr) load_q(0);
+  auto keep = [&](const uint2& a) {
+    if constexpr (Elem<E>::IS_F16)
+      big = Elem<E>::max2(big, Elem<E>::max2(a.x & 0x7fff7fffu, a.y & 0x7fff7fffu));
+  };
+  auto rotate = [&](const PapRaw<SRC>* raw, uint2* out) {
+    uint64_t a[2], b[2];
+    raw[0].get(a);
+    raw[1].get(b);
+    if (p.rotate) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) turn.apply(e, a[e], b[e]);
+    }
+    out[0] = pap_round<E>(a);
+    out[1] = pap_round<E>(b);
+    keep(out[0]);
+    keep(out[1]);
+  };
+  if (row >= 0) {
+    E* pv = static_cast<E*>(p.pv) + row + part * 4;
+    if constexpr (std::is_same<typename PapRaw<SRC>::T, E>::value) {   // no rounding: the bits as they are
+      *reinterpret_cast<uint2*>(pv) = vr[0].r;
+      *reinterpret_cast<uint2*>(pv + H2) = vr[1].r;
+      keep(vr[0].r);
+      keep(vr[1].r);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        uint64_t f[2];
+        vr[e].get(f);
+        const uint2 r = pap_round<E>(f);
+        *reinterpret_cast<uint2*>(pv + e * H2) = r;
+        keep(r);
+      }
+    }
+    rotate(kr, k);
+    E* pk = static_cast<E*>(p.pk) + row + part * 4;
+    *reinterpret_cast<uint2*>(pk) = k[0];
+    *reinterpret_cast<uint2*>(pk + H2) = k[1];
+  }
+  if (p.q == nullptr) return;
+  E* qo = static_cast<E*>(p.q_out) + (tok * p.Hkv + g) * p.G * D + part * 4;
+  for (int h0 = 0;;) {
+#pragma unroll
+    for (int h = 0; h < QB; ++h) {
+      if (h0 + h < p.G) {
+        uint2 y[2];
+        rotate(qr[h], y);
+        *reinterpret_cast<uint2*>(qo + (h0 + h) * D) = y[0];
+        *reinterpret_cast<uint2*>(qo + (h0 + h) * D + H2) = y[1];
+      }
+    }
+    h0 += QB;
+    if (h0 >= p.G) break;
+    load_q(h0);
+  }
+}
+// Values that rounded to an infinity: |v| >= 65520 in an fp16 pool.
 template <typename E>
-__device__ __forceinline__ void pap_store4(E* dst, const float* f) {
-  *reinterpret_cast<uint2*>(dst) = make_uint2(Elem<E>::pack(f[0], f[1]), Elem<E>::pack(f[2], f[3]));
+__device__ __forceinline__ void pap_report(const PagedAppendParams& p, uint32_t big) {
+  if constexpr (Elem<E>::IS_F16)
+    if ((big & 0xffffu) == (Elem<E>::INF2 & 0xffffu) || (big >> 16) == (Elem<E>::INF2 >> 16))
+      report_error(p.status, DEV_ERR_FP16_RANGE, 614);
+}
+
+// The page of a sequence's page number page_no, or -1 (reported) where there is none.
+__device__ __forceinline__ int pap_page(const PagedAppendParams& p, int b, int page_no) {
+  const int page = page_no < p.width ? p.table[(long long)b * p.table_stride + page_no] : -1;
+  if (page >= 0 && page < p.n_pages) return page;
+  report_error(p.status, DEV_ERR_BOUNDS, 613);
+  return -1;
+}
+
+// Bounds of 4 channels of a page and head: widened by [l, h] (old), or set to it.
+template <typename E>
+__device__ __forceinline__ void pap_bounds(const PagedAppendParams& p, long long at, bool old, uint2 l, uint2 h) {
+  uint2* lo = reinterpret_cast<uint2*>(static_cast<E*>(p.k_lo) + at);
+  uint2* hi = reinterpret_cast<uint2*>(static_cast<E*>(p.k_hi) + at);
+  if (old) {
+    const uint2 a = *lo, b = *hi;
+    l = make_uint2(Elem<E>::min2(l.x, a.x), Elem<E>::min2(l.y, a.y));
+    h = make_uint2(Elem<E>::max2(h.x, b.x), Elem<E>::max2(h.y, b.y));
+  }
+  *lo = l;
+  *hi = h;
+}
+
+template <typename E, int D, int SRC>
+__global__ void __launch_bounds__(PAP_STEP_THREADS) paged_append_step_kernel(const __grid_constant__ PagedAppendParams p) {
+  pdl_wait();
+  pdl_trigger();
+  constexpr int PARTS = D / 8;
+  const long long i = (long long)blockIdx.x * PAP_STEP_THREADS + threadIdx.x;
+  const int part = (int)(i % PARTS), g = (int)(i / PARTS % p.Hkv);
+  const long long bl = i / PARTS / p.Hkv;
+  if (bl >= p.B) return;
+  const int b = (int)bl;
+  const int pos = p.start[b] + p.start_add;
+  if (pos < 0) {   // refused whole: neither keys nor queries of this sequence
+    report_error(p.status, DEV_ERR_BOUNDS, 612);
+    return;
+  }
+  const int in_page = pos & ((1 << p.ps_log2) - 1);
+  const int page = p.pk != nullptr ? pap_page(p, b, pos >> p.ps_log2) : -1;
+  PapTurn<4> turn;
+  if (p.rotate) turn.at(p, pos, part * 4);
+  uint2 k[2];
+  uint32_t big = 0;
+  pap_token<E, D, SRC>(p, turn, b,
+                       page < 0 ? -1 : (long long)page * p.page_stride + g * p.head_stride + (long long)in_page * p.row_stride,
+                       g, part, k, big);
+  pap_report<E>(p, big);
+  if (p.k_lo != nullptr && page >= 0) {
+    const long long at = ((long long)page * p.Hkv + g) * D + part * 4;
+    pap_bounds<E>(p, at, in_page > 0, k[0], k[0]);
+    pap_bounds<E>(p, at + D / 2, in_page > 0, k[1], k[1]);
+  }
 }
 
 // New tokens of sequence b and its first token row; 0 tokens (and a report) where cu_new does
@@ -148,198 +382,279 @@ __device__ __forceinline__ int pap_runs(const PagedAppendParams& p, int b) {
   return ((s + n - 1) >> p.ps_log2) - (s >> p.ps_log2) + 1;
 }
 
-template <typename E, int D>
-__global__ void __launch_bounds__(PAP_THREADS) paged_append_kernel(const __grid_constant__ PagedAppendParams p) {
+// 4 source elements in shared memory as two packed fp32 pairs
+template <int SRC>
+__device__ __forceinline__ void pap_get4(const uint8_t* s, uint64_t* f) {
+  if constexpr (SRC == PDT_F32) {
+    const float4 a = *reinterpret_cast<const float4*>(s);
+    f[0] = f2_pack(a.x, a.y);
+    f[1] = f2_pack(a.z, a.w);
+  } else {
+    PapRaw<SRC> raw;
+    raw.r = *reinterpret_cast<const uint2*>(s);
+    raw.get(f);
+  }
+}
+// Rounded to the pool's type; big: the largest magnitudes rounded so far (fp16 pools)
+template <typename E>
+__device__ __forceinline__ uint2 pap_round(const uint64_t* f, uint32_t& big) {
+  const uint2 a = pap_round<E>(f);
+  if constexpr (Elem<E>::IS_F16)
+    big = Elem<E>::max2(big, Elem<E>::max2(a.x & 0x7fff7fffu, a.y & 0x7fff7fffu));
+  return a;
+}
+
+// what a stage's rows need besides their bytes
+struct PapMeta {
+  long long row;     // element offset of the first row in the pool (head included), or -1: no place
+  int tok, pos;      // first token row and position
+  int rows, g;
+  int page;
+  int old, last;     // the page was begun by an earlier call; the run's last stage
+};
+
+template <typename E, int D, int SRC>
+__global__ void __launch_bounds__(PAP_THREADS, PAP_PER_SM)
+    paged_append_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant__ CUtensorMap mapV,
+                        const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ PagedAppendParams p) {
+  constexpr int H2 = D / 2, PARTS = D / 8;      // threads of a row: 4 pairs each
+  constexpr int ESZ = SRC == PDT_F32 ? 4 : 2;
+  constexpr int HB = D * ESZ;                   // bytes of a head
+  constexpr int NW = PAP_THREADS / 32;
+  extern __shared__ __align__(128) uint8_t pap_smem[];   // stages of k, v [chunk][D] and q [chunk / 8][G][8][D]
+  __shared__ __align__(8) uint32_t red[2][PAP_CONSUMERS];
+  __shared__ uint64_t full[PAP_STAGES], empty[PAP_STAGES], sync_bar;
+  __shared__ PapMeta metas[PAP_STAGES];
+  __shared__ int abort_flag;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (tid == 0) {
+    for (int i = 0; i < PAP_STAGES; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], PAP_CONSUMERS / 32);
+    }
+    mbar_init(&sync_bar, PAP_CONSUMERS / 32);
+    abort_flag = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&mapK);
+    tma_prefetch_desc(&mapV);
+    tma_prefetch_desc(&mapQ);
+  }
+  __syncthreads();
   pdl_wait();
   pdl_trigger();
-  constexpr int H2 = D / 2;
-  constexpr int RC = 1024 / D;         // rows per chunk: 128 key items of 4 pairs
-  constexpr int PARTS = H2 / 4;
-  __shared__ float2 cs_tab[RC][H2];
-  __shared__ float red[4][2][D];
-  __shared__ int wsum[PAP_THREADS / 32];
-  __shared__ int pick[2];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int g = blockIdx.y;
 
-  // 1. this CTA's run: sequence b and its page number within the sequence's new tokens
-  int b, run;
-  if (p.cu_new == nullptr) {
-    b = blockIdx.x;
-    run = 0;
-    if (pap_runs(p, b) == 0) return;
-  } else {
-    const int per = (p.B + PAP_THREADS - 1) / PAP_THREADS;
-    const int b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
-    int mine = 0;
-    for (int i = b0; i < b1; ++i) mine += pap_runs(p, i);
-    int inc = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int up = __shfl_up_sync(0xffffffffu, inc, o);
-      if (lane >= o) inc += up;
-    }
-    if (lane == 31) wsum[warp] = inc;
-    if (tid == 0) pick[0] = -1;
-    __syncthreads();
-    int before = inc - mine;
-    for (int w = 0; w < warp; ++w) before += wsum[w];
-    const int u = blockIdx.x;
-    if (u >= before && u < before + mine) {
-      int i = b0, left = u - before;
-      for (; i < b1; ++i) {
-        const int r = pap_runs(p, i);
-        if (left < r) break;
-        left -= r;
-      }
-      pick[0] = i;
-      pick[1] = left;
-    }
-    __syncthreads();
-    b = pick[0];
-    run = pick[1];
-    if (b < 0) return;   // past the last run (the grid is sized for the most there can be)
-  }
-  int row0;
-  const int n = pap_count(p, b, &row0);
-  const int s0 = p.start[b] + p.start_add;
-  const int ps = 1 << p.ps_log2;
-  const int page_no = (s0 >> p.ps_log2) + run;            // page index within the sequence
-  // (64-bit: the last page of the position range may end at 2^31)
-  const int pos0 = run == 0 ? s0 : page_no << p.ps_log2;
-  const long long pos1 = min((long long)s0 + n, ((long long)page_no + 1) << p.ps_log2);
-  const int rows = (int)(pos1 - pos0);
-  const int tok0 = row0 + (pos0 - s0);
-  int page = -1;
-  if (p.pk != nullptr) {
-    if (page_no < p.width) page = p.table[(long long)b * p.table_stride + page_no];
-    if (page < 0 || page >= p.n_pages) {   // nowhere to write: reported, queries still rotated
-      if (tid == 0) report_error(p.status, DEV_ERR_BOUNDS, 613);
-      page = -1;
-    }
-  }
-  E* pk = static_cast<E*>(p.pk) + (page < 0 ? 0 : (long long)page * p.page_stride + g * p.head_stride);
-  E* pv = static_cast<E*>(p.pv) + (page < 0 ? 0 : (long long)page * p.page_stride + g * p.head_stride);
-  const int in_page = pos0 & (ps - 1);
+  const int stage_bytes = p.chunk * HB * ((p.q != nullptr ? p.G : 0) + (p.k != nullptr ? 2 : 0));
+  int stg = 0;
+  uint32_t phase = 0;
 
-  float lo[8], hi[8];
+  if (warp == NW - 1) {
+    // ------------------------------ producer warp ------------------------------
+    int b = 0, run = blockIdx.x / p.Hkv, g = blockIdx.x % p.Hkv, filled = 0;   // run: counted from sequence b's first
+    bool ok = true;
+    // moves b to the sequence that holds the run, 32 sequences at a step; false past the last
+    auto seek = [&]() {
+      for (; b < p.B; b += 32) {
+        const int c = b + lane < p.B ? pap_runs(p, b + lane) : 0;
+        int inc = c;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    lo[e] = INFINITY;
-    hi[e] = -INFINITY;
-  }
-  const int item = tid & 127, irow = item / PARTS, part = item % PARTS;
-  for (int c0 = 0; c0 < rows; c0 += RC) {
-    const int nr = min(RC, rows - c0);
-    if (p.rotate) {
-      for (int i = tid; i < nr * H2; i += PAP_THREADS) {
-        const int r = i / H2, j = i % H2;
-        const double t = (double)(pos0 + c0 + r) * p.turns[j];
-        float sn, cs;
-        sincospif(2.f * (float)(t - rint(t)), &sn, &cs);
-        cs_tab[r][j] = make_float2(cs, sn);
-      }
-      __syncthreads();
-    }
-    // the pair elements x1 (j..j+3) and x2 (j+H2..) of row r, rotated
-    auto rot = [&](int r, int j, float* x1, float* x2) {
-      if (!p.rotate) return;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float2 t = cs_tab[r][j + e];
-        const float a = x1[e] * t.x - x2[e] * t.y;
-        x2[e] = x2[e] * t.x + x1[e] * t.y;
-        x1[e] = a;
-      }
-    };
-    auto guard = [&](const float* x1, const float* x2) {
-      if constexpr (Elem<E>::IS_F16) {
-        f16_range_guard<4>(x1, p.status, 614);
-        f16_range_guard<4>(x2, p.status, 614);
-      }
-    };
-    if (page >= 0 && irow < nr) {
-      const long long src = (long long)(tok0 + c0 + irow);
-      const long long dst = (in_page + c0 + irow) * p.row_stride + part * 4;
-      float x1[4], x2[4];
-      if (tid < 128) {
-        const long long at = src * p.k_stride + g * D + part * 4;
-        pap_load4(p, p.k, at, x1);
-        pap_load4(p, p.k, at + H2, x2);
-        rot(irow, part * 4, x1, x2);
-        guard(x1, x2);
-        pap_store4<E>(pk + dst, x1);
-        pap_store4<E>(pk + dst + H2, x2);
-        // rounding keeps the order, so the bounds of the stored keys are the rounded bounds
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          lo[e] = fminf(lo[e], x1[e]);
-          hi[e] = fmaxf(hi[e], x1[e]);
-          lo[e + 4] = fminf(lo[e + 4], x2[e]);
-          hi[e + 4] = fmaxf(hi[e + 4], x2[e]);
+        for (int o = 1; o < 32; o <<= 1) {
+          const int up = __shfl_up_sync(0xffffffffu, inc, o);
+          if (lane >= o) inc += up;
         }
-      } else {
-        const long long at = src * p.v_stride + g * D + part * 4;
-        pap_load4(p, p.v, at, x1);
-        pap_load4(p, p.v, at + H2, x2);
-        guard(x1, x2);
-        pap_store4<E>(pv + dst, x1);
-        pap_store4<E>(pv + dst + H2, x2);
+        const unsigned hit = __ballot_sync(0xffffffffu, inc > run);
+        if (hit != 0) {
+          const int l = __ffs(hit) - 1;
+          run -= __shfl_sync(0xffffffffu, inc - c, l);
+          b += l;
+          return true;
+        }
+        run -= __shfl_sync(0xffffffffu, inc, 31);
+      }
+      return false;
+    };
+    while (ok && seek()) {
+      int row0;
+      const int n = pap_count(p, b, &row0), s0 = p.start[b] + p.start_add;
+      const int page_no = (s0 >> p.ps_log2) + run;          // page number within the sequence
+      const int pos0 = run == 0 ? s0 : page_no << p.ps_log2;
+      // (64-bit: the last page of the position range may end at 2^31)
+      const int rows = (int)(min((long long)s0 + n, ((long long)page_no + 1) << p.ps_log2) - pos0);
+      const int in_page = pos0 & ((1 << p.ps_log2) - 1);
+      const int page = p.pk != nullptr ? pap_page(p, b, page_no) : -1;
+      const long long base = (long long)page * p.page_stride + g * p.head_stride + (long long)in_page * p.row_stride;
+      const int tok0 = row0 + (pos0 - s0);
+      for (int c0 = 0; c0 < rows && ok; c0 += p.chunk) {
+        const int nr = min(p.chunk, rows - c0);
+        if (filled >= PAP_STAGES) ok = mbar_wait(&empty[stg], phase ^ 1u, &abort_flag, p.status, 615);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        uint8_t* sk = pap_smem + stg * stage_bytes;
+        uint8_t* sv = sk + (p.k != nullptr ? p.chunk * HB : 0);
+        uint8_t* sq = sv + (p.k != nullptr ? p.chunk * HB : 0);
+        const int boxes = (nr + PAP_BOX - 1) / PAP_BOX, q_heads = p.q != nullptr ? p.G : 0;
+        if (lane == 0) {
+          PapMeta& m = metas[stg];
+          m.row = page < 0 ? -1 : base + c0 * p.row_stride;
+          m.tok = tok0 + c0;
+          m.pos = pos0 + c0;
+          m.rows = nr;
+          m.g = g;
+          m.page = page;
+          m.old = in_page > 0;
+          m.last = c0 + nr >= rows;
+          mbar_arrive_expect_tx(&full[stg], boxes * PAP_BOX * HB * ((page >= 0 ? 2 : 0) + q_heads));
+        }
+        __syncwarp();
+        const int per_box = q_heads + 2;   // per 8 tokens the boxes of the query heads, k and v, [8][D] each
+        for (int x = lane; x < boxes * per_box; x += 32) {
+          const int bx = x / per_box, h = x % per_box, tok = tok0 + c0 + bx * PAP_BOX;
+          if (h < q_heads) {
+            tma_load_2d(sq + (bx * p.G + h) * PAP_BOX * HB, &mapQ, &full[stg], (g * p.G + h) * D, tok);
+          } else if (page >= 0) {
+            tma_load_2d((h == q_heads ? sk : sv) + bx * PAP_BOX * HB, h == q_heads ? &mapK : &mapV, &full[stg], g * D,
+                        tok);
+          }
+        }
+        ++filled;
+        if (++stg == PAP_STAGES) {
+          stg = 0;
+          phase ^= 1u;
+        }
+      }
+      g += gridDim.x % p.Hkv;
+      run += gridDim.x / p.Hkv;
+      if (g >= p.Hkv) {
+        g -= p.Hkv;
+        ++run;
       }
     }
-    if (p.q != nullptr) {
-      const int per_head = nr * PARTS;
-      for (int i = tid; i < p.G * per_head; i += PAP_THREADS) {
-        const int h = g * p.G + i / per_head, r = (i % per_head) / PARTS, j = (i % PARTS) * 4;
-        const long long tok = tok0 + c0 + r;
-        float x1[4], x2[4];
-        const long long at = tok * p.q_stride + h * D + j;
-        pap_load4(p, p.q, at, x1);
-        pap_load4(p, p.q, at + H2, x2);
-        rot(r, j, x1, x2);
-        guard(x1, x2);
-        E* qo = static_cast<E*>(p.q_out) + (tok * p.Hkv * p.G + h) * D + j;
-        pap_store4<E>(qo, x1);
-        pap_store4<E>(qo + H2, x2);
+    if (lane == 0) {
+      // the loads in flight land before the CTA can exit (also when the consumers gave up) ...
+      int back = stg;
+      uint32_t back_phase = phase;
+      for (int k = min(filled, PAP_STAGES); k > 0; --k) {
+        if (--back < 0) {
+          back = PAP_STAGES - 1;
+          back_phase ^= 1u;
+        }
+        mbar_wait(&full[back], back_phase, nullptr, p.status, 617);
+      }
+      // ... and one more stage, without rows, ends the consumers' walk
+      if (ok && filled >= PAP_STAGES) ok = mbar_wait(&empty[stg], phase ^ 1u, &abort_flag, p.status, 616);
+      if (ok) {
+        metas[stg].rows = 0;
+        mbar_arrive(&full[stg]);
       }
     }
-    if (p.rotate) __syncthreads();   // the next chunk rewrites the table
+    return;
   }
 
-  // 2. page bounds: over the run's rows, and over what an earlier call wrote when the run
-  //    does not begin the page
-  if (p.k_lo != nullptr && page >= 0) {
+  // ------------------------------ consumer warps ------------------------------
+  constexpr int PAIRS = D / 2, ROWS_AT_ONCE = PAP_CONSUMERS / PAIRS;   // bounds: threads by two channels and row
+  constexpr uint32_t LO0 = Elem<E>::INF2, HI0 = Elem<E>::INF2 | 0x80008000u;
+  uint32_t big = 0, lo = LO0, hi = HI0, sync_phase = 0;
+  auto group_sync = [&]() {   // bounded, so that a warp that gave up holds no one for long
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sync_bar);
+    const bool r = mbar_wait(&sync_bar, sync_phase & 1u, &abort_flag, p.status, 618);
+    ++sync_phase;
+    return __all_sync(0xffffffffu, r) != 0;
+  };
+  for (;;) {
+    bool ok = mbar_wait(&full[stg], phase, &abort_flag, p.status, 619);
+    ok = __all_sync(0xffffffffu, ok);
+    if (!ok) break;
+    const PapMeta m = metas[stg];
+    if (m.rows == 0) break;
+    uint8_t* sk = pap_smem + stg * stage_bytes;
+    const uint8_t* sv = sk + (p.k != nullptr ? p.chunk * HB : 0);
+    const uint8_t* sq = sv + (p.k != nullptr ? p.chunk * HB : 0);
+    const bool bounds = p.k_lo != nullptr && m.page >= 0;
+    for (int i = tid; i < m.rows * PARTS; i += PAP_CONSUMERS) {
+      const int r = i / PARTS, part = i % PARTS;
+      const int at = r * HB + part * 4 * ESZ;
+      PapTurn<4> turn;
+      if (p.rotate) turn.at(p, m.pos + r, part * 4);
+      auto rotate = [&](const uint8_t* s, uint2* out) {
+        uint64_t a[2], c[2];
+        pap_get4<SRC>(s, a);
+        pap_get4<SRC>(s + H2 * ESZ, c);
+        if (p.rotate) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
+          for (int e = 0; e < 2; ++e) turn.apply(e, a[e], c[e]);
+        }
+        out[0] = pap_round<E>(a, big);
+        out[1] = pap_round<E>(c, big);
+      };
+      if (m.page >= 0) {
+        const long long dst = m.row + r * p.row_stride + part * 4;
+        uint2 y[2];
+        uint64_t f[2];
 #pragma unroll
-      for (int o = PARTS; o < 32; o <<= 1) {
-        lo[e] = fminf(lo[e], __shfl_xor_sync(0xffffffffu, lo[e], o));
-        hi[e] = fmaxf(hi[e], __shfl_xor_sync(0xffffffffu, hi[e], o));
+        for (int e = 0; e < 2; ++e) {
+          pap_get4<SRC>(sv + at + e * H2 * ESZ, f);
+          *reinterpret_cast<uint2*>(static_cast<E*>(p.pv) + dst + e * H2) = pap_round<E>(f, big);
+        }
+        rotate(sk + at, y);
+        *reinterpret_cast<uint2*>(static_cast<E*>(p.pk) + dst) = y[0];
+        *reinterpret_cast<uint2*>(static_cast<E*>(p.pk) + dst + H2) = y[1];
+        if (bounds) {   // the stored key, over its source (which this thread alone reads)
+          *reinterpret_cast<uint2*>(sk + at) = y[0];
+          *reinterpret_cast<uint2*>(sk + at + H2 * ESZ) = y[1];
+        }
+      }
+      if (p.q != nullptr) {
+        E* qo = static_cast<E*>(p.q_out) + ((long long)(m.tok + r) * p.Hkv + m.g) * p.G * D + part * 4;
+        const uint8_t* qs = sq + ((r / PAP_BOX) * p.G * PAP_BOX + r % PAP_BOX) * HB + part * 4 * ESZ;
+#pragma unroll 2
+        for (int h = 0; h < p.G; ++h) {
+          uint2 y[2];
+          rotate(qs + h * PAP_BOX * HB, y);
+          *reinterpret_cast<uint2*>(qo + h * D) = y[0];
+          *reinterpret_cast<uint2*>(qo + h * D + H2) = y[1];
+        }
       }
     }
-    if (tid < 128 && lane < PARTS) {
+    if (bounds) {
+      if (!group_sync()) break;
+      // channels 2c, 2c + 1: of the 4 of a part, at 16-bit steps behind the part's first byte
+      const int c = tid % PAIRS, half = c / (H2 / 2), x = c % (H2 / 2);
+      const uint8_t* col = sk + half * H2 * ESZ + (x / 2) * 4 * ESZ + (x % 2) * 4;
+      for (int r = tid / PAIRS; r < m.rows; r += ROWS_AT_ONCE) {
+        const uint32_t k = *reinterpret_cast<const uint32_t*>(col + r * HB);
+        lo = Elem<E>::min2(lo, k);
+        hi = Elem<E>::max2(hi, k);
+      }
+      fence_proxy_async_smem();   // the kept keys were written through the generic proxy
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&empty[stg]);   // this warp is done with the stage
+    if (bounds && m.last) {
+      // over the run's rows, and over what an earlier call wrote when the run does not begin
+      // the page (red is free again by the next stage's group_sync)
+      red[0][tid] = lo;
+      red[1][tid] = hi;
+      lo = LO0;
+      hi = HI0;
+      if (!group_sync()) break;
+      if (tid < D / 4) {
+        uint2 l = *reinterpret_cast<const uint2*>(&red[0][2 * tid]), h = *reinterpret_cast<const uint2*>(&red[1][2 * tid]);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const int d = (e < 4 ? 0 : H2) + lane * 4 + (e & 3);
-        red[warp][0][d] = lo[e];
-        red[warp][1][d] = hi[e];
+        for (int k = 1; k < ROWS_AT_ONCE; ++k) {
+          const uint2 l2 = *reinterpret_cast<const uint2*>(&red[0][k * PAIRS + 2 * tid]);
+          const uint2 h2 = *reinterpret_cast<const uint2*>(&red[1][k * PAIRS + 2 * tid]);
+          l = make_uint2(Elem<E>::min2(l.x, l2.x), Elem<E>::min2(l.y, l2.y));
+          h = make_uint2(Elem<E>::max2(h.x, h2.x), Elem<E>::max2(h.y, h2.y));
+        }
+        pap_bounds<E>(p, ((long long)m.page * p.Hkv + m.g) * D + tid * 4, m.old != 0, l, h);
       }
     }
-    __syncthreads();
-    if (tid < D) {
-      const long long at = ((long long)page * p.Hkv + g) * D + tid;
-      E* blo = static_cast<E*>(p.k_lo) + at;
-      E* bhi = static_cast<E*>(p.k_hi) + at;
-      float l = fminf(fminf(red[0][0][tid], red[1][0][tid]), fminf(red[2][0][tid], red[3][0][tid]));
-      float h = fmaxf(fmaxf(red[0][1][tid], red[1][1][tid]), fmaxf(red[2][1][tid], red[3][1][tid]));
-      if (in_page > 0) {
-        l = fminf(l, (float)*blo);
-        h = fmaxf(h, (float)*bhi);
-      }
-      *blo = (E)l;
-      *bhi = (E)h;
+    if (++stg == PAP_STAGES) {
+      stg = 0;
+      phase ^= 1u;
     }
   }
+  pap_report<E>(p, big);
 }
 
 // ----------------------------------------------------------------------------------------
@@ -781,7 +1096,7 @@ __device__ __noinline__ void pa_arrive_rest(const PagedAttnParams& p, int b, int
     t = 0;
     if (++g == p.Hkv) {
       g = 0;
-      ++b;
+      b = min(b + 1, p.B - 1);
     }
   }
 }
@@ -908,9 +1223,9 @@ __global__ void __launch_bounds__(PaShape<D, NHB>::THREADS, 1)
     for (int k = 0; k < GROUPS; ++k) {
       int left = share(k) - before;
       if (left < 0 || left >= mine) continue;
-      for (int i = b0;; ++i) {
+      for (int i = b0; i < b1; ++i) {
         const int nt = pa_tiles(p, pa_len(p, i)).n_tiles;
-        if (left < nt * p.Hkv) {
+        if (left < nt * p.Hkv || i + 1 == b1) {
           start[k][0] = i;
           start[k][1] = left / nt;
           start[k][2] = left % nt;
@@ -989,7 +1304,7 @@ __global__ void __launch_bounds__(PaShape<D, NHB>::THREADS, 1)
         first = true;
         if (++g == p.Hkv) {
           g = 0;
-          ++b;
+          b = min(b + 1, p.B - 1);   // (the last step is past the share's end)
           sq = pa_tiles(p, next_len);
           next_len = b + 1 < p.B ? pa_len(p, b + 1) : 0;
         }

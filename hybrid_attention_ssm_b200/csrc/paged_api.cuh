@@ -103,7 +103,7 @@ int paged_dispatch(const hymba_paged_kv* kv, F&& f) {
 }
 
 // Enqueue the append kernel; p holds everything but the pool's fields.
-int launch_paged_append(const hymba_paged_kv* kv, PagedAppendParams& p, float rope_base, cudaStream_t st) {
+int launch_paged_append(const hymba_paged_kv* kv, PagedAppendParams& p, float rope_base, int sms, cudaStream_t st) {
   p.Hkv = kv->n_kv_heads;
   p.n_pages = kv->n_pages;
   p.ps_log2 = log2_int(kv->page_size);
@@ -118,21 +118,73 @@ int launch_paged_append(const hymba_paged_kv* kv, PagedAppendParams& p, float ro
   }
   p.rotate = rope_base > 0.f ? 1 : 0;
   const int h2 = kv->head_dim / 2;
-  for (int j = 0; p.rotate && j < h2; ++j)
-    p.turns[j] = std::exp2(-std::log2((double)rope_base) * j / h2) * 0.15915494309189535;
-  // the most runs there can be: a sequence of n tokens touches at most (n + 2 ps - 2) / ps
+  for (int j = 0; p.rotate && j < h2; ++j) {   // the turn's fraction in units of 2^-64
+    const double t = std::exp2(-std::log2((double)rope_base) * j / h2) * 0.15915494309189535;
+    p.turns[j] = (unsigned long long)((t - std::floor(t)) * 18446744073709551616.0);
+  }
+  // the most runs there can be (only a bound: the kernel counts them): a sequence of n tokens touches at most (n + 2 ps - 2) / ps
   // pages, and no more than it has tokens
-  long long runs = p.B;
-  if (p.cu_new != nullptr) {
-    runs = ((long long)p.T + (long long)p.B * (2 * kv->page_size - 2)) / kv->page_size;
-    if (runs > p.T) runs = p.T;
+  long long runs = ((long long)p.T + (long long)p.B * (2 * kv->page_size - 2)) / kv->page_size;
+  if (runs > p.T) runs = p.T;
+  const bool step = p.cu_new == nullptr;
+  const long long items = step ? (long long)p.B * (kv->head_dim / 8) * p.Hkv : runs * p.Hkv;
+  if (items > 0x7fffffff) return fail(HYMBA_ERR_UNSUPPORTED, "%d tokens of %d sequences: too many for one call", p.T, p.B);
+  const int threads = step ? PAP_STEP_THREADS : PAP_THREADS;
+  const int blocks = step ? cdiv(items, threads) : (int)std::min<long long>(items, PAP_PER_SM * sms);
+  const int esz = p.src == PDT_F32 ? 4 : 2, head_bytes = kv->head_dim * esz;
+  const int row_bytes = ((p.q != nullptr ? p.G : 0) + (p.k != nullptr ? 2 : 0)) * head_bytes;
+  // a stage: one 4-pair item per consumer thread, in whole boxes, within its bytes
+  p.chunk = std::max(PAP_BOX, std::min({kv->page_size, PAP_CONSUMERS * 8 / kv->head_dim,
+                                        PAP_STAGE_BYTES / row_bytes / PAP_BOX * PAP_BOX}));
+  const size_t smem = step ? 0 : (size_t)PAP_STAGES * p.chunk * row_bytes;
+  // tensor maps of the source rows [T, heads * D], boxes of one head
+  CUtensorMap mk, mv, mq;
+  auto map_rows = [&](CUtensorMap* m, const void* base, int heads, long long stride) {
+    const CUtensorMapDataType dt = p.src == PDT_F32   ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                   : p.src == PDT_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                                      : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    const uint64_t dims[2] = {(uint64_t)heads * kv->head_dim, (uint64_t)p.T};
+    const uint64_t str[1] = {(uint64_t)stride * esz};
+    const uint32_t box[2] = {(uint32_t)kv->head_dim, (uint32_t)PAP_BOX};
+    return make_map(m, base, dt, 2, dims, str, box, CU_TENSOR_MAP_SWIZZLE_NONE);
+  };
+  if (!step) {
+    if (p.n_slices > 1) return fail(HYMBA_ERR_UNSUPPORTED, "split-K slices go with one token per sequence");
+    if (p.k != nullptr) {
+      HY_TRY(map_rows(&mk, p.k, p.Hkv, p.k_stride));
+      HY_TRY(map_rows(&mv, p.v, p.Hkv, p.v_stride));
+    }
+    if (p.q != nullptr) HY_TRY(map_rows(&mq, p.q, p.Hkv * p.G, p.q_stride));
+    if (p.k == nullptr) mk = mv = mq;
+    if (p.q == nullptr) mq = mk;
   }
   return paged_dispatch(kv, [&](auto e, auto d) {
-    prof_begin("paged_append", st);
-    HY_CUDA(launch_pdl(paged_append_kernel<decltype(e), decltype(d)::value>, dim3((unsigned)runs, kv->n_kv_heads),
-                       dim3(PAP_THREADS), 0, st, p));
-    prof_end(st);
-    return (int)HYMBA_OK;
+    using E = decltype(e);
+    constexpr int D = decltype(d)::value;
+    auto run = [&](auto src) {
+      constexpr int SRC = decltype(src)::value;
+      if (step) {
+        prof_begin("paged_append", st);
+        HY_CUDA(launch_pdl(paged_append_step_kernel<E, D, SRC>, dim3((unsigned)blocks), dim3(threads), 0, st, p));
+        prof_end(st);
+        return (int)HYMBA_OK;
+      }
+      auto kern = paged_append_kernel<E, D, SRC>;
+      static bool attr[64] = {false};
+      int dcur = 0;
+      HY_CUDA(cudaGetDevice(&dcur));
+      if (!attr[dcur & 63]) {
+        HY_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, PAP_SMEM_MAX));
+        attr[dcur & 63] = true;
+      }
+      prof_begin("paged_append", st);
+      HY_CUDA(launch_pdl(kern, dim3((unsigned)blocks), dim3(threads), smem, st, mk, mv, mq, p));
+      prof_end(st);
+      return (int)HYMBA_OK;
+    };
+    if (p.src == PDT_F32) return run(std::integral_constant<int, PDT_F32>{});
+    if (p.src == PDT_F16) return run(std::integral_constant<int, PDT_F16>{});
+    return run(std::integral_constant<int, PDT_BF16>{});
   });
 }
 
@@ -249,7 +301,7 @@ int hymba_paged_append(const hymba_paged_kv* kv, const hymba_page_table* table, 
   p.table = table->pages; p.table_stride = table->stride; p.width = table->width;
   p.B = table->batch; p.T = n_tokens; p.G = G;
   p.status = reinterpret_cast<DevStatus*>(ws);
-  return launch_paged_append(kv, p, rope_base, (cudaStream_t)stream);
+  return launch_paged_append(kv, p, rope_base, dev->sms, (cudaStream_t)stream);
 }
 
 int hymba_paged_select(const hymba_paged_kv* kv, const hymba_page_table* table, const int* seq_lens, const void* q,

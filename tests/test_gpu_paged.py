@@ -1,9 +1,10 @@
 """The paged cache operators on the GPU against the 64-bit definitions in paged_ref.
 
 Bounds, derived from the arithmetic (u16 = eps / 2 of the type, u = 2^-24):
-  append     the angle in turns is reduced in 64 bits and rounded to fp32 (2 pi 2^-25 in angle),
-             sincospif is good to 2 ulp, two products and a sum: 8 u (|x1| + |x2|) and one
-             rounding to the pool's type (u16 |ref|, 2^-25 in fp16's subnormals)
+  append     the angle is a phase modulo 2^64 (2^-32 of a turn when it is used), its sine and
+             cosine come from fp32 polynomials (at most 4 u each), two products and a sum:
+             8 u (|x1| + |x2|) and one rounding to the pool's type (u16 |ref|, 2^-25 in
+             fp16's subnormals)
   attention  scores: D products in fp32 accumulation, each step off by at most 2 u of the
              running size S = scale sum|q k|, then the scale and the subtraction of the maximum:
              d = (2 D + 8) u S in the exponent's argument, for numerator and denominator alike;
@@ -326,6 +327,18 @@ def test_append(Hq, Hkv, D, ps, dt, src, base, layout):
         r = run_append(ps, Hq, Hkv, D, dt, src, start, new, base, bounds, with_q=bounds, layout=layout)
         assert r["status"] == H.OK
         check_append(r, ps, dt, start, new, base)
+
+
+@pytest.mark.parametrize("Hq,Hkv,D,ps,dt,src", [(4, 2, 64, 16, torch.float16, torch.float32),
+                                                (16, 1, 128, 32, torch.bfloat16, torch.float32)])
+def test_append_many_short_sequences(Hq, Hkv, D, ps, dt, src):
+    """More sequences than a warp looks through at once, runs of them without new tokens, more
+    items than CTAs; the widest group's rows need the largest stage."""
+    start = [(i * 13) % 70 for i in range(500)]
+    new = [0 if i % 7 in (1, 2) or 100 <= i < 170 else (i * 5) % 40 for i in range(500)]
+    r = run_append(ps, Hq, Hkv, D, dt, src, start, new, 10000.0)
+    assert r["status"] == H.OK
+    check_append(r, ps, dt, start, new, 10000.0)
 
 
 def test_append_one_token_each_and_far_positions():
