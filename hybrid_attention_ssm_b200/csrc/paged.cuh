@@ -681,6 +681,11 @@ __device__ __forceinline__ double q_scale() {   // 2^1000 or 2^880: |up| stays b
   return Elem<E>::IS_F16 ? __hiloint2double((1023 + 1000) << 20, 0) : __hiloint2double((1023 + 880) << 20, 0);
 }
 
+// A cluster of 1 to 8 CTAs serves a (sequence, kv head): each scores a share of the pages, 8
+// channels per lane, into the first CTA's shared memory, and that CTA ranks them: a radix
+// selection from the top digit down, on keys (the scores' bits in an order-preserving form)
+// rebased to the smallest one so that the first digit already spreads them, until at most 32
+// candidates share the digits of the last page taken; a warp ranks those.
 struct PagedSelectParams {
   const void *k_lo, *k_hi;   // [n_pages, Hkv, D]
   const void* q;             // [B] rows of Hq*D
@@ -689,7 +694,6 @@ struct PagedSelectParams {
   long long table_stride;
   const int* lens;
   int width, B, Hkv, G, n_pages, ps_log2, n_first, n_last, top;
-  unsigned long long* keys;  // [B, Hkv, width] scores in an order-preserving integer form
   int* page_idx;             // [B, Hkv, top]
   DevStatus* status;
 };
@@ -699,219 +703,273 @@ __device__ __forceinline__ int paged_len(int len, int width, int ps_log2) {
   return len < 0 ? 0 : (int)min((long long)len, cap);
 }
 
-constexpr int PSC_PAGES = 64;     // pages per warp
-constexpr int PSC_THREADS = 128;
+constexpr int PSEL_THREADS = 256;
+constexpr int PSEL_WARPS = PSEL_THREADS / 32;
+
+__device__ __forceinline__ void st_cluster_u64(uint32_t addr, unsigned long long v) {
+  asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(addr), "l"(v) : "memory");
+}
 
 template <typename E, int D>
-__global__ void __launch_bounds__(PSC_THREADS) paged_score_kernel(const PagedSelectParams p) {
+__global__ void __launch_bounds__(PSEL_THREADS, 2)
+    paged_select_kernel(const __grid_constant__ PagedSelectParams p, int cluster) {
+  constexpr int LPP = D / 8;          // lanes per page
+  constexpr int PPI = 32 / LPP;       // pages per warp at a time
+  extern __shared__ unsigned long long psel_keys[];   // one per page, in the cluster's first CTA
+  __shared__ unsigned long long red[2][PSEL_WARPS], cand_key[32], last_key;
+  __shared__ int hist[256], found[2], cand_idx[32], n_cand, last_idx, wsum[PSEL_WARPS];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int rank = blockIdx.x % cluster, bg = blockIdx.x / cluster, b = bg / p.Hkv, g = bg % p.Hkv;
+  const int d0 = (lane % LPP) * 8, sub = lane / LPP;
   pdl_wait();
   pdl_trigger();
-  constexpr int LPP = D / 8;          // lanes per page: 8 dims each
-  constexpr int PPI = 32 / LPP;       // pages per warp and iteration
-  const int lane = threadIdx.x & 31;
-  const int n_chunks = (p.width + PSC_PAGES - 1) / PSC_PAGES;
-  const long long w = (long long)blockIdx.x * (PSC_THREADS / 32) + (threadIdx.x >> 5);
-  const int g = (int)(w % p.Hkv), chunk = (int)(w / p.Hkv % n_chunks);
-  const long long bl = w / p.Hkv / n_chunks;
-  if (bl >= p.B) return;
-  const int b = (int)bl;
+  constexpr int QB = 8;   // query heads whose loads are in flight together, with the length's
+  const E* q = static_cast<const E*>(p.q) + b * p.q_stride + (long long)g * p.G * D + d0;
+  uint4 qr[QB];
+#pragma unroll
+  for (int h = 0; h < QB; ++h)
+    if (h < p.G) qr[h] = *reinterpret_cast<const uint4*>(q + h * D);
   const int raw_len = p.lens[b];
   const int len = paged_len(raw_len, p.width, p.ps_log2);
-  if (len != raw_len && lane == 0) report_error(p.status, DEV_ERR_BOUNDS, 621);
-  const int n = (int)(((long long)len + (1 << p.ps_log2) - 1) >> p.ps_log2);
-  const int j0 = chunk * PSC_PAGES, j1 = min(n, j0 + PSC_PAGES);
-  if (j0 >= n) return;
-  const int d0 = (lane % LPP) * 8, sub = lane / LPP;
-  double up[8], dn[8];
-#pragma unroll
-  for (int e = 0; e < 8; ++e) up[e] = dn[e] = 0.0;
-  const E* q = static_cast<const E*>(p.q) + b * p.q_stride + (long long)g * p.G * D + d0;
-  for (int h = 0; h < p.G; ++h) {
-    const uint4 r = *reinterpret_cast<const uint4*>(q + h * D);
-    const uint32_t wds[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float2 f = Elem<E>::unpack(wds[e / 2]);
-      const float x = (e & 1) ? f.y : f.x;
-      if (x > 0.f) up[e] += (double)x;
-      else dn[e] += (double)x;
-    }
-  }
-  const double qs = q_scale<E>();
-#pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    up[e] *= qs;
-    dn[e] *= qs;
-  }
-  unsigned long long* keys = p.keys + ((long long)b * p.Hkv + g) * p.width;
-#pragma unroll 2
-  for (int j = j0; j < j1; j += PPI) {
-    const int jj = j + sub;
-    double s = 0.0;
-    if (jj < j1) {
-      int page = p.table[(long long)b * p.table_stride + jj];
-      if (page < 0 || page >= p.n_pages) {   // ranked last; reading it is reported by the attention too
-        report_error(p.status, DEV_ERR_BOUNDS, 622);
-        s = -__hiloint2double(0x7fe00000, 0);
-      } else {
-        const long long at = ((long long)page * p.Hkv + g) * D + d0;
-        const uint4 a = *reinterpret_cast<const uint4*>(static_cast<const E*>(p.k_hi) + at);
-        const uint4 c = *reinterpret_cast<const uint4*>(static_cast<const E*>(p.k_lo) + at);
-        const uint32_t hw[4] = {a.x, a.y, a.z, a.w}, lw[4] = {c.x, c.y, c.z, c.w};
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          s = fma(up[e], raw_double<E>((hw[e / 2] >> (16 * (e & 1))) & 0xffffu), s);
-          s = fma(dn[e], raw_double<E>((lw[e / 2] >> (16 * (e & 1))) & 0xffffu), s);
-        }
-      }
-    }
-#pragma unroll
-    for (int o = LPP / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    if (jj < j1 && lane % LPP == 0) {
-      const unsigned long long u = (unsigned long long)__double_as_longlong(s + 0.0);   // -0 becomes +0
-      keys[jj] = (u >> 63) ? ~u : u | 0x8000000000000000ull;
-    }
-  }
-}
-
-// The top pages of one (sequence, kv head): the first n_first and last n_last are taken, and
-// of the rest the largest keys, ties to the lowest index; the list is written in ascending
-// order and filled up with -1.  Radix selection from the top digit down, on keys rebased to
-// the smallest one so that the first digit already spreads them: `base` and `bits` bound the
-// bin that holds the last page taken, `need` counts the pages still to take from it.
-constexpr int PPK_THREADS = 512;
-template <int THREADS>
-__device__ __forceinline__ unsigned long long block_red_u64(unsigned long long v, bool take_max,
-                                                            unsigned long long* sh) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    const unsigned long long w = __shfl_xor_sync(0xffffffffu, v, o);
-    v = take_max ? max(v, w) : min(v, w);
-  }
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = v;
-  __syncthreads();
-  v = sh[0];
-  for (int i = 1; i < THREADS / 32; ++i) v = take_max ? max(v, sh[i]) : min(v, sh[i]);
-  return v;
-}
-
-__global__ void __launch_bounds__(PPK_THREADS) paged_pick_kernel(const PagedSelectParams p) {
-  pdl_wait();
-  pdl_trigger();
-  extern __shared__ unsigned long long ppk_keys[];
-  __shared__ unsigned long long red[PPK_THREADS / 32];
-  __shared__ int hist[256];
-  __shared__ int found[2];
-  __shared__ int wsum[PPK_THREADS / 32][2];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int bg = blockIdx.x, b = bg / p.Hkv;
-  const int len = paged_len(p.lens[b], p.width, p.ps_log2);
+  if (len != raw_len && tid == 0) report_error(p.status, DEV_ERR_BOUNDS, 621);
   const int n = (int)(((long long)len + (1 << p.ps_log2) - 1) >> p.ps_log2);
   int* out = p.page_idx + (long long)bg * p.top;
-  if (n <= p.top) {   // every page
-    for (int i = tid; i < p.top; i += PPK_THREADS) out[i] = i < n ? i : -1;
+  if (n <= p.top) {   // every page (the whole cluster takes this branch)
+    if (rank == 0)
+      for (int i = tid; i < p.top; i += PSEL_THREADS) out[i] = i < n ? i : -1;
     return;
   }
-  const unsigned long long* keys = p.keys + (long long)bg * p.width;
-  // n > top >= n_first + n_last: the forced pages do not overlap
-  const int f0 = p.n_first, f1 = n - p.n_last;
-  unsigned long long mn = ~0ull, mx = 0;
-  for (int i = tid; i < n; i += PPK_THREADS) {
-    const unsigned long long k = keys[i];
-    ppk_keys[i] = k;
-    if (i >= f0 && i < f1) {
-      mn = min(mn, k);
-      mx = max(mx, k);
-    }
-  }
-  mn = block_red_u64<PPK_THREADS>(mn, false, red);
-  mx = block_red_u64<PPK_THREADS>(mx, true, red);
-  int need = p.top - p.n_first - p.n_last;
-  unsigned long long base = mn;
-  int bits = 64 - __clzll((long long)(mx - mn));
-  bool whole = need == 0;   // every key >= base is taken (need == 0: none, base above all)
-  if (need == 0) base = mx + 1;   // (mx < 2^64 - 1: scores are finite)
-  while (!whole && bits > 0) {
-    const int shift = max(bits - 8, 0);
-    for (int i = tid; i < 256; i += PPK_THREADS) hist[i] = 0;
-    __syncthreads();
-    for (int i = f0 + tid; i < f1; i += PPK_THREADS) {
-      const unsigned long long r = ppk_keys[i] - base;
-      if (ppk_keys[i] >= base && (bits == 64 || (r >> bits) == 0)) atomicAdd(&hist[(int)(r >> shift)], 1);
-    }
-    __syncthreads();
-    if (warp == 0) {   // the bin where the count from the top reaches `need`
-      int c[8], s = 0;
+
+  // 1. scores of this CTA's share, a chunk of up to 32 pages per warp at a time
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  {
+    const int share = (n + cluster - 1) / cluster, s0 = min(n, rank * share), s1 = min(n, s0 + share);
+    int chunk = 32;   // small shares: fewer, so that every warp has some
+    while (chunk > PPI && chunk * PSEL_WARPS >= 2 * share) chunk >>= 1;
+    double up[8], dn[8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        c[e] = hist[255 - (lane * 8 + e)];
-        s += c[e];
-      }
-      int inc = s;
+    for (int e = 0; e < 8; ++e) up[e] = dn[e] = 0.0;
+    for (int h0 = 0; h0 < p.G; h0 += QB) {
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int u = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o) inc += u;
-      }
-      int above = inc - s;
-      if (above < need && inc >= need) {
+      for (int h = 0; h < QB; ++h) {
+        if (h0 + h >= p.G) break;
+        const uint4 r = h0 == 0 ? qr[h] : *reinterpret_cast<const uint4*>(q + (h0 + h) * D);
+        const uint32_t w[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          if (above < need && above + c[e] >= need) {
-            found[0] = 255 - (lane * 8 + e);
-            found[1] = above;
-          }
-          above += c[e];
+        for (int e = 0; e < 4; ++e) {
+          const float2 f = Elem<E>::unpack(w[e]);
+          up[2 * e] += (double)fmaxf(f.x, 0.f);
+          up[2 * e + 1] += (double)fmaxf(f.y, 0.f);
+          dn[2 * e] += (double)fminf(f.x, 0.f);
+          dn[2 * e + 1] += (double)fminf(f.y, 0.f);
         }
       }
     }
-    __syncthreads();
-    const int d = found[0];
-    need -= found[1];
-    whole = hist[d] == need;
-    base += (unsigned long long)d << shift;
-    bits = shift;
-    __syncthreads();
-  }
-  // taken: forced, key above the bin's single value, or (not whole) among the first `need`
-  // equal to it
-  const int per = (n + PPK_THREADS - 1) / PPK_THREADS;
-  const int i0 = min(n, tid * per), i1 = min(n, i0 + per);
-  int gt = 0, eq = 0;
-  for (int i = i0; i < i1; ++i) {
-    const unsigned long long k = ppk_keys[i];
-    if (i < f0 || i >= f1 || k > base || (whole && k == base)) ++gt;
-    else if (k == base) ++eq;
-  }
-  int ig = gt, ie = eq;
+    const double qs = q_scale<E>();
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int a = __shfl_up_sync(0xffffffffu, ig, o), c = __shfl_up_sync(0xffffffffu, ie, o);
-    if (lane >= o) {
-      ig += a;
-      ie += c;
+    for (int e = 0; e < 8; ++e) {
+      up[e] *= qs;
+      dn[e] *= qs;
+    }
+    const uint32_t keys0 = smem_cluster_addr(psel_keys, 0);
+    // the first CTA has started before its shared memory is written
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    for (int j0 = s0 + warp * chunk; j0 < s1; j0 += PSEL_WARPS * chunk) {
+      const int nj = min(chunk, s1 - j0);
+      int entry = -1;
+      if (lane < nj) {
+        entry = p.table[(long long)b * p.table_stride + j0 + lane];
+        if (entry < 0 || entry >= p.n_pages) {   // not in the pool: ranked last
+          report_error(p.status, DEV_ERR_BOUNDS, 622);
+          entry = -1;
+        }
+      }
+      constexpr int UN = 4;   // page groups whose loads are in flight together
+      for (int i0 = 0; i0 < nj; i0 += UN * PPI) {
+        int page[UN];
+        uint4 hi[UN], lo[UN];
+#pragma unroll
+        for (int u = 0; u < UN; ++u) {
+          page[u] = __shfl_sync(0xffffffffu, entry, (i0 + u * PPI + sub) & 31);
+          const long long at = ((long long)max(page[u], 0) * p.Hkv + g) * D + d0;   // (page 0 in the place of none)
+          hi[u] = *reinterpret_cast<const uint4*>(static_cast<const E*>(p.k_hi) + at);
+          lo[u] = *reinterpret_cast<const uint4*>(static_cast<const E*>(p.k_lo) + at);
+        }
+#pragma unroll
+        for (int u = 0; u < UN; ++u) {
+          const uint32_t hw[4] = {hi[u].x, hi[u].y, hi[u].z, hi[u].w}, lw[4] = {lo[u].x, lo[u].y, lo[u].z, lo[u].w};
+          double s = 0.0, t = 0.0;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            s = fma(up[e], raw_double<E>((hw[e / 2] >> (16 * (e & 1))) & 0xffffu), s);
+            t = fma(dn[e], raw_double<E>((lw[e / 2] >> (16 * (e & 1))) & 0xffffu), t);
+          }
+          s += t;
+#pragma unroll
+          for (int o = LPP / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+          const int i = i0 + u * PPI + sub;
+          if (i < nj && lane % LPP == 0) {
+            const unsigned long long v = (unsigned long long)__double_as_longlong(s + 0.0);   // -0 becomes +0
+            st_cluster_u64(keys0 + (j0 + i) * 8,
+                           page[u] < 0 ? 0ull : ((v >> 63) ? ~v : v | 0x8000000000000000ull));
+          }
+        }
+      }
     }
   }
-  if (lane == 31) {
-    wsum[warp][0] = ig;
-    wsum[warp][1] = ie;
+  cluster_sync();
+  if (rank != 0) return;
+
+  // 2. the range of the keys of the pages that are not forced (n > top >= n_first + n_last: the
+  //    forced ones do not overlap)
+  const int f0 = p.n_first, f1 = n - p.n_last;
+  unsigned long long mn = ~0ull, mx = 0;
+  // (the loops of the selection run once a call: unrolled, they would cost more in instruction
+  // fetches than they save)
+#pragma unroll 1
+  for (int i = f0 + tid; i < f1; i += PSEL_THREADS) {
+    mn = min(mn, psel_keys[i]);
+    mx = max(mx, psel_keys[i]);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    mn = min(mn, __shfl_xor_sync(0xffffffffu, mn, o));
+    mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+  }
+  if (lane == 0) {
+    red[0][warp] = mn;
+    red[1][warp] = mx;
+  }
+  hist[tid] = 0;
+  if (tid == 0) n_cand = 0;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < PSEL_WARPS; ++w) {
+    mn = min(mn, red[0][w]);
+    mx = max(mx, red[1][w]);
+  }
+
+  // 3. the last page taken: (key, number), no other page that is taken ranks lower.  The pages
+  //    with base <= key < base + 2^bits are still undecided, `need` of them are taken.
+  int need = p.top - p.n_first - p.n_last, count = f1 - f0;
+  unsigned long long base = mn;
+  int bits = 64 - __clzll((long long)(mx - mn));
+  auto undecided = [&](unsigned long long k) { return k >= base && (bits == 64 || ((k - base) >> bits) == 0); };
+  if (need == 0) {
+    if (tid == 0) {
+      last_key = ~0ull;
+      last_idx = -1;
+    }
+  } else {
+    while (count > 32 && bits > 0) {
+      const int shift = max(bits - 8, 0);
+#pragma unroll 1
+      for (int i = f0 + tid; i < f1; i += PSEL_THREADS) {
+        const unsigned long long k = psel_keys[i];
+        if (undecided(k)) atomicAdd(&hist[(int)((k - base) >> shift)], 1);
+      }
+      __syncthreads();
+      if (warp == 0) {   // the bin where the count from the top reaches `need`
+        int c[8], s = 0;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          c[e] = hist[255 - (lane * 8 + e)];
+          s += c[e];
+        }
+        int inc = s;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int u = __shfl_up_sync(0xffffffffu, inc, o);
+          if (lane >= o) inc += u;
+        }
+        int above = inc - s;
+        if (above < need && inc >= need) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            if (above < need && above + c[e] >= need) {
+              found[0] = 255 - (lane * 8 + e);
+              found[1] = above;
+            }
+            above += c[e];
+          }
+        }
+      }
+      __syncthreads();
+      const int d = found[0];
+      need -= found[1];
+      count = hist[d];
+      base += (unsigned long long)d << shift;
+      bits = shift;
+      __syncthreads();
+      hist[tid] = 0;
+      __syncthreads();
+    }
+    if (count <= 32) {   // rank the candidates
+#pragma unroll 1
+      for (int i = f0 + tid; i < f1; i += PSEL_THREADS) {
+        const unsigned long long k = psel_keys[i];
+        if (undecided(k)) {
+          const int at = atomicAdd(&n_cand, 1);
+          cand_key[at] = k;
+          cand_idx[at] = i;
+        }
+      }
+      __syncthreads();
+      if (warp == 0) {
+        const bool in = lane < count;
+        const unsigned long long k = in ? cand_key[lane] : 0;
+        const int idx = in ? cand_idx[lane] : 0;
+        int above = 0;
+#pragma unroll 1
+        for (int o = 0; o < count; ++o) {
+          const unsigned long long k2 = __shfl_sync(0xffffffffu, k, o);
+          const int i2 = __shfl_sync(0xffffffffu, idx, o);
+          above += k2 > k || (k2 == k && i2 < idx) ? 1 : 0;
+        }
+        if (in && above == need - 1) {
+          last_key = k;
+          last_idx = idx;
+        }
+      }
+    } else if (warp == 0) {   // more than 32 pages of one score: the need-th of them
+      int seen = 0;
+      for (int i = f0; i < f1; i += 32) {
+        const bool eq = i + lane < f1 && psel_keys[i + lane] == base;
+        const unsigned m = __ballot_sync(0xffffffffu, eq);
+        if (eq && seen + __popc(m & ((1u << lane) - 1)) == need - 1) {
+          last_key = base;
+          last_idx = i + lane;
+        }
+        seen += __popc(m);
+      }
+    }
   }
   __syncthreads();
-  int bg_ = ig - gt, be = ie - eq;
-  for (int k = 0; k < warp; ++k) {
-    bg_ += wsum[k][0];
-    be += wsum[k][1];
-  }
-  for (int i = i0; i < i1; ++i) {
-    const unsigned long long k = ppk_keys[i];
-    if (i < f0 || i >= f1 || k > base || (whole && k == base)) {
-      out[bg_ + min(be, need)] = i;
-      ++bg_;
-    } else if (k == base) {
-      if (be < need) out[bg_ + be] = i;
-      ++be;
-    }
+
+  // 4. the list: every warp writes the pages of its stretch in order
+  const unsigned long long lk = last_key;
+  const int li = last_idx;
+  auto taken = [&](int i) {
+    if (i >= n) return false;
+    if (i < f0 || i >= f1) return true;
+    const unsigned long long k = psel_keys[i];
+    return k > lk || (k == lk && i <= li);
+  };
+  const int stretch = (n + PSEL_THREADS - 1) / PSEL_THREADS * 32, i0 = warp * stretch, i1 = min(n, i0 + stretch);
+  int mine = 0;
+#pragma unroll 1
+  for (int i = i0; i < i1; i += 32) mine += __popc(__ballot_sync(0xffffffffu, taken(i + lane)));
+  if (lane == 0) wsum[warp] = mine;
+  __syncthreads();
+  int at = 0;
+#pragma unroll 1
+  for (int w = 0; w < warp; ++w) at += wsum[w];
+#pragma unroll 1
+  for (int i = i0; i < i1; i += 32) {
+    const bool t = taken(i + lane);
+    const unsigned m = __ballot_sync(0xffffffffu, t);
+    if (t) out[at + __popc(m & ((1u << lane) - 1))] = i + lane;
+    at += __popc(m);
   }
 }
 

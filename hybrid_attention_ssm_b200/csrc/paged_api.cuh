@@ -7,18 +7,15 @@ namespace {
 constexpr int PAGED_MAX_SELECT_WIDTH = 16384;   // one CTA ranks a sequence's pages in shared memory
 
 struct PagedWs {
-  size_t arrived, part, keys, total;
+  size_t arrived, part, total;
 };
 // The attention's part counters follow the status word (hymba_workspace_init zeroes both, and
-// every call leaves the counters at zero).  Its parts and the selection's keys share the rest:
-// calls on one workspace follow one another.
-PagedWs paged_layout(int head_dim, int n_kv_heads, int group, int batch, int max_pages) {
+// every call leaves the counters at zero), then its parts.  The other calls use the status word.
+PagedWs paged_layout(int head_dim, int group) {
   PagedWs w;
   w.arrived = 256;
-  w.part = w.keys = align256(w.arrived + (size_t)PA_MAX_GRID * sizeof(unsigned));
-  const size_t attn = w.part + (size_t)PA_MAX_GRID * 2 * group * (head_dim + 4) * 4;
-  const size_t sel = w.keys + (size_t)batch * n_kv_heads * (size_t)max_pages * 8;
-  w.total = align256(attn > sel ? attn : sel);
+  w.part = align256(w.arrived + (size_t)PA_MAX_GRID * sizeof(unsigned));
+  w.total = align256(w.part + (size_t)PA_MAX_GRID * 2 * group * (head_dim + 4) * 4);
   return w;
 }
 
@@ -255,7 +252,7 @@ int hymba_paged_workspace_size(const hymba_paged_kv* kv, int batch, int n_q_head
   int G = 0;
   HY_TRY(paged_group(kv, n_q_heads, &G));
   if (bytes == nullptr || batch < 1 || max_pages < 1) return fail(HYMBA_ERR_INVALID_ARG, "paged workspace arguments");
-  *bytes = paged_layout(kv->head_dim, kv->n_kv_heads, G, batch, max_pages).total;
+  *bytes = paged_layout(kv->head_dim, G).total;   // (what the calls need does not grow with the batch)
   return HYMBA_OK;
 }
 
@@ -320,12 +317,9 @@ int hymba_paged_select(const hymba_paged_kv* kv, const hymba_page_table* table, 
     return fail(HYMBA_ERR_INVALID_ARG, "seq_lens / page_idx / q");
   if (n_first < 0 || n_last < 0 || top_pages < 1 || (long long)n_first + n_last > top_pages)
     return fail(HYMBA_ERR_INVALID_ARG, "top_pages %d with %d first and %d last", top_pages, n_first, n_last);
-  const PagedWs L = paged_layout(kv->head_dim, kv->n_kv_heads, G, table->batch, table->width);
-  HY_TRY(check_paged_ws(ws, ws_bytes, L.total));
+  HY_TRY(check_paged_ws(ws, ws_bytes, 256));
   DeviceInfo* dev = nullptr;
   HY_TRY(device_info(&dev));
-  cudaStream_t st = (cudaStream_t)stream;
-  uint8_t* wsb = static_cast<uint8_t*>(ws);
   PagedSelectParams p{};
   p.k_lo = kv->k_lo; p.k_hi = kv->k_hi;
   p.q = q; p.q_stride = q_stride;
@@ -334,31 +328,41 @@ int hymba_paged_select(const hymba_paged_kv* kv, const hymba_page_table* table, 
   p.B = table->batch; p.Hkv = kv->n_kv_heads; p.G = G; p.n_pages = kv->n_pages;
   p.ps_log2 = log2_int(kv->page_size);
   p.n_first = n_first; p.n_last = n_last; p.top = top_pages;
-  p.keys = reinterpret_cast<unsigned long long*>(wsb + L.keys);
   p.page_idx = page_idx;
   p.status = reinterpret_cast<DevStatus*>(ws);
-  const long long warps = (long long)p.B * p.Hkv * cdiv(p.width, PSC_PAGES);
-  const long long blocks = (warps + PSC_THREADS / 32 - 1) / (PSC_THREADS / 32);
-  if (blocks > 0x7fffffff || (long long)p.B * p.Hkv > 0x7fffffff) return fail(HYMBA_ERR_UNSUPPORTED, "batch too large");
-  HY_TRY(paged_dispatch(kv, [&](auto e, auto d) {
-    prof_begin("paged_score", st);
-    HY_CUDA(launch_pdl(paged_score_kernel<decltype(e), decltype(d)::value>, dim3((unsigned)blocks), dim3(PSC_THREADS),
-                       0, st, p));
-    prof_end(st);
+  // the largest cluster that leaves the CTAs of the call resident at once (four per SM) and at
+  // least 64 pages to a CTA
+  const long long lists = (long long)p.B * p.Hkv;
+  int cluster = 8;
+  while (cluster > 1 && (lists * cluster > 4 * 148 || p.width < 64 * cluster)) cluster >>= 1;
+  if (lists * cluster > 0x7fffffff) return fail(HYMBA_ERR_UNSUPPORTED, "batch too large");
+  return paged_dispatch(kv, [&](auto e, auto d) {
+    auto kern = paged_select_kernel<decltype(e), decltype(d)::value>;
+    static bool attr[64] = {false};
+    int dcur = 0;
+    HY_CUDA(cudaGetDevice(&dcur));
+    if (!attr[dcur & 63]) {
+      HY_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, PAGED_MAX_SELECT_WIDTH * 8));
+      attr[dcur & 63] = true;
+    }
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)(lists * cluster));
+    cfg.blockDim = dim3(PSEL_THREADS);
+    cfg.dynamicSmemBytes = (size_t)p.width * 8;
+    cfg.stream = (cudaStream_t)stream;
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = cluster;
+    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 2;
+    prof_begin("paged_select", cfg.stream);
+    HY_CUDA(cudaLaunchKernelEx(&cfg, kern, p, cluster));
+    prof_end(cfg.stream);
     return (int)HYMBA_OK;
-  }));
-  static bool attr[64] = {false};
-  int dcur = 0;
-  HY_CUDA(cudaGetDevice(&dcur));
-  if (!attr[dcur & 63]) {
-    HY_CUDA(cudaFuncSetAttribute(paged_pick_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 PAGED_MAX_SELECT_WIDTH * 8));
-    attr[dcur & 63] = true;
-  }
-  prof_begin("paged_pick", st);
-  HY_CUDA(launch_pdl(paged_pick_kernel, dim3(p.B * p.Hkv), dim3(PPK_THREADS), (size_t)p.width * 8, st, p));
-  prof_end(st);
-  return HYMBA_OK;
+  });
 }
 
 int hymba_paged_attention(const hymba_paged_kv* kv, const hymba_page_table* table, const int* seq_lens, const void* q,
@@ -381,7 +385,7 @@ int hymba_paged_attention(const hymba_paged_kv* kv, const hymba_page_table* tabl
     return fail(HYMBA_ERR_INVALID_ARG, "n_meta %d, window %d (meta tokens go with a window)", n_meta, window);
   if (page_idx != nullptr && (window > 0 || top_pages < 1 || !aligned4(page_idx)))
     return fail(HYMBA_ERR_INVALID_ARG, "a page list goes without a window, with top_pages >= 1");
-  const PagedWs L = paged_layout(kv->head_dim, kv->n_kv_heads, G, 1, 1);
+  const PagedWs L = paged_layout(kv->head_dim, G);
   HY_TRY(check_paged_ws(ws, ws_bytes, L.total));
   DeviceInfo* dev = nullptr;
   HY_TRY(device_info(&dev));

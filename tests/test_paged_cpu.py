@@ -102,7 +102,7 @@ def test_append_refusals(kw, code):
     (dict(first=-1), H.ERR_INVALID_ARG), (dict(last=-1), H.ERR_INVALID_ARG), (dict(first=2, last=2), H.ERR_INVALID_ARG),
     (dict(first=2 ** 31 - 1, last=2 ** 31 - 1), H.ERR_INVALID_ARG),
     (dict(kv=cache(k_lo=None, k_hi=None)), H.ERR_INVALID_ARG),
-    (dict(tb=table(width=16385, stride=16385)), H.ERR_UNSUPPORTED), (dict(wsb=1024), H.ERR_WORKSPACE)])
+    (dict(tb=table(width=16385, stride=16385)), H.ERR_UNSUPPORTED), (dict(wsb=128), H.ERR_WORKSPACE)])
 def test_select_refusals(kw, code):
     assert select(**kw) == code
 
@@ -128,7 +128,7 @@ def test_workspace_size_grows_with_what_needs_it():
     a = size(1, 4, 1)
     assert a % 256 == 0 and a >= 148 * 2 * 2 * 68 * 4
     assert size(1, 4, 1, head_dim=128) > a and size(1, 32, 1) > a
-    assert size(64, 4, 16384) >= 64 * 2 * 16384 * 8
+    assert size(64, 4, 16384) == a     # neither the batch nor the lengths matter
     for kw, args in ((dict(), (0, 4, 1)), (dict(), (1, 5, 1)), (dict(), (1, 4, 0)), (dict(page_size=20), (1, 4, 1))):
         assert H.lib().hymba_paged_workspace_size(ctypes.byref(cache(**kw)), *args, ctypes.byref(n)) != H.OK
 
