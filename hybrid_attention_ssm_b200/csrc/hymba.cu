@@ -1308,36 +1308,43 @@ int hymba_mixer_prefill_host(const hymba_layer_cfg* cfg, const hymba_layer_weigh
 // The decode step; positions == NULL: every sequence at `position`; otherwise sequence b at
 // positions[b] (device memory), each <= `position`, which sizes the attention's key splits.
 // norm_out != NULL: the final split-K sum also writes norm_out = RMSNorm(out) * norm_gain.
+// paged != NULL: the keys and values are in a paged cache (kv is NULL, positions is not).
 static int decode_impl(const hymba_layer_cfg* cfg, const hymba_layer_weights* w, const hymba_bf16* x, int B,
                        int position, const int* positions, hymba_kv_cache* kv, float* ssm_state,
                        float* conv_state, const hymba_bf16* residual, hymba_bf16* out, void* ws, size_t ws_bytes,
                        hymba_stream stream, const float* norm_gain = nullptr, float norm_eps = 0.f,
-                       hymba_bf16* norm_out = nullptr) {
+                       hymba_bf16* norm_out = nullptr, const PagedDecode* paged = nullptr) {
   HY_TRY(check_cfg(cfg));
   DeviceInfo* dev = nullptr;
   HY_TRY(device_info(&dev));
   const Dims m = dims_of(cfg);
   if (B < 1) return fail(HYMBA_ERR_INVALID_ARG, "batch %d", B);
   HY_TRY(check_weights(w, m, false));
-  if (x == nullptr || out == nullptr || kv == nullptr || ssm_state == nullptr || conv_state == nullptr ||
-      !aligned16(x) || !aligned16(out) || !aligned16(conv_state) || !aligned16(ssm_state))
+  if (x == nullptr || out == nullptr || (kv == nullptr && paged == nullptr) || ssm_state == nullptr ||
+      conv_state == nullptr || !aligned16(x) || !aligned16(out) || !aligned16(conv_state) || !aligned16(ssm_state))
     return fail(HYMBA_ERR_INVALID_ARG, "x/out/kv/state pointer");
-  if (position < m.M) return fail(HYMBA_ERR_INVALID_ARG, "position %d < n_meta %d", position, m.M);
-  if (kv->batch < B || kv->n_kv_heads != m.Hkv || kv->head_dim != m.D)
-    return fail(HYMBA_ERR_INVALID_ARG, "kv cache shape");
   const bool global = cfg->is_global != 0;
-  if (global) {
-    if (kv->kind != HYMBA_CACHE_GLOBAL || kv->k == nullptr || position >= kv->max_tokens)
-      return fail(HYMBA_ERR_INVALID_ARG, "global cache / position %d >= max_tokens", position);
+  if (paged != nullptr) {
+    HY_TRY(check_paged_decode(*paged, cfg));
   } else {
-    if (kv->kind != HYMBA_CACHE_SWA || kv->ring_k == nullptr || (m.M > 0 && kv->meta_k == nullptr) ||
-        kv->window != m.W || kv->n_meta != m.M)
-      return fail(HYMBA_ERR_INVALID_ARG, "SWA cache");
+    if (position < m.M) return fail(HYMBA_ERR_INVALID_ARG, "position %d < n_meta %d", position, m.M);
+    if (kv->batch < B || kv->n_kv_heads != m.Hkv || kv->head_dim != m.D)
+      return fail(HYMBA_ERR_INVALID_ARG, "kv cache shape");
+    if (global) {
+      if (kv->kind != HYMBA_CACHE_GLOBAL || kv->k == nullptr || position >= kv->max_tokens)
+        return fail(HYMBA_ERR_INVALID_ARG, "global cache / position %d >= max_tokens", position);
+    } else {
+      if (kv->kind != HYMBA_CACHE_SWA || kv->ring_k == nullptr || (m.M > 0 && kv->meta_k == nullptr) ||
+          kv->window != m.W || kv->n_meta != m.M)
+        return fail(HYMBA_ERR_INVALID_ARG, "SWA cache");
+    }
   }
-  const int max_keys = decode_max_keys(cfg, kv->max_tokens);
-  const DecodeWs L = decode_layout(m, B, global, max_keys);
+  const DecodeWs L = paged != nullptr ? paged_decode_base(m, B)
+                                      : decode_layout(m, B, global, decode_max_keys(cfg, kv->max_tokens));
+  const PagedDecodeWs PL = paged != nullptr ? paged_decode_layout(m, B, paged->top_pages) : PagedDecodeWs{};
+  const size_t need = paged != nullptr ? PL.total : L.total;
   if (ws == nullptr || (reinterpret_cast<uintptr_t>(ws) & 255u)) return fail(HYMBA_ERR_INVALID_ARG, "workspace");
-  if (ws_bytes < L.total) return fail(HYMBA_ERR_WORKSPACE, "workspace %zu < %zu bytes", ws_bytes, L.total);
+  if (ws_bytes < need) return fail(HYMBA_ERR_WORKSPACE, "workspace %zu < %zu bytes", ws_bytes, need);
   cudaStream_t st = (cudaStream_t)stream;
   uint8_t* wsb = static_cast<uint8_t*>(ws);
   DevStatus* status = reinterpret_cast<DevStatus*>(ws);
@@ -1364,7 +1371,16 @@ static int decode_impl(const hymba_layer_cfg* cfg, const hymba_layer_weights* w,
     c.p.status = status;
     HY_TRY(run_gemm(c, *dev, st));
   }
-  // 2. conv step, RoPE of q and the new k, the new k/v into the cache
+  // 2. conv step, RoPE of q and the new k, the new k/v into the cache (a paged cache: the conv
+  //    step only; the append follows on the side stream)
+  SideStream* side = nullptr;
+  HY_TRY(side_stream(&side));
+  ForkGuard fork_guard(side, st);
+  if (paged != nullptr) {
+    HY_CUDA(cudaEventRecord(side->fork, st));
+    HY_CUDA(cudaStreamWaitEvent(side->s, side->fork, 0));
+    fork_guard.open = true;
+  }
   {
     DecPrepParams pp;
     pp.proj = f32(L.proj);
@@ -1379,19 +1395,20 @@ static int decode_impl(const hymba_layer_cfg* cfg, const hymba_layer_weights* w,
     pp.conv_b = w->conv_b;
     pp.conv_state = conv_state;
     pp.xc = bf(L.xc);
-    pp.Hq = m.Hq; pp.Hkv = m.Hkv; pp.p = position; pp.write_kv = own_kv ? 1 : 0;
+    pp.Hq = paged != nullptr ? 0 : m.Hq; pp.Hkv = m.Hkv; pp.p = position;
+    pp.write_kv = own_kv && paged == nullptr ? 1 : 0;
     pp.positions = positions;
     pp.max_position = position;
-    pp.is_global = global ? 1 : 0; pp.M = m.M; pp.W = m.W; pp.Lmax = kv->max_tokens;
-    pp.ring_k = reinterpret_cast<__half*>(kv->ring_k);
-    pp.ring_v = reinterpret_cast<__half*>(kv->ring_v);
-    pp.full_k = reinterpret_cast<__half*>(kv->k);
-    pp.full_v = reinterpret_cast<__half*>(kv->v);
+    pp.is_global = global ? 1 : 0; pp.M = m.M; pp.W = m.W; pp.Lmax = kv != nullptr ? kv->max_tokens : 0;
+    pp.ring_k = kv != nullptr ? reinterpret_cast<__half*>(kv->ring_k) : nullptr;
+    pp.ring_v = kv != nullptr ? reinterpret_cast<__half*>(kv->ring_v) : nullptr;
+    pp.full_k = kv != nullptr ? reinterpret_cast<__half*>(kv->k) : nullptr;
+    pp.full_v = kv != nullptr ? reinterpret_cast<__half*>(kv->v) : nullptr;
     pp.qrot = f32(L.qrot);
     pp.status = status;
     pp.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)m.D));
     fill_rope_theta(pp.rope_theta, cfg->rope_base);
-    const int n_rope = B * (m.Hq + (own_kv ? m.Hkv : 0)) * 32;
+    const int n_rope = paged != nullptr ? 0 : B * (m.Hq + (own_kv ? m.Hkv : 0)) * 32;
     prof_begin("decode_prep", st);
     HY_CUDA(launch_pdl(decode_prep_kernel, dim3(pp.conv_blocks + cdiv(n_rope, 256)), dim3(256), 0, st, pp));
     prof_end(st);
@@ -1400,11 +1417,13 @@ static int decode_impl(const hymba_layer_cfg* cfg, const hymba_layer_weights* w,
   //    The two branches are independent from here to the norm: the attention runs on the
   //    side stream beside x_proj and the SSM step (both chains are latency-bound kernels
   //    that leave most of the GPU idle), joined before the norm.
-  SideStream* side = nullptr;
-  HY_TRY(side_stream(&side));
-  ForkGuard fork_guard(side, st);
   int attn_items = 0;   // the attention's work items (its grid is min(items, 3 per SM))
-  {
+  if (paged != nullptr) {
+    attn_items = 3 * dev->sms;   // its CTAs take every SM's shared memory
+    HY_TRY(launch_paged_decode(*paged, cfg, m, B, positions, f32(L.proj), L.in_split, own_kv, PL, wsb, f32(L.o), *dev,
+                               side->s));
+    HY_CUDA(cudaEventRecord(side->join, side->s));
+  } else {
     const cudaStream_t ast = side->s;
     DecAttnParams ap;
     ap.qrot = f32(L.qrot);
@@ -1593,6 +1612,27 @@ int hymba_mixer_decode_ragged(const hymba_layer_cfg* cfg, const hymba_layer_weig
     return fail(HYMBA_ERR_INVALID_ARG, "positions pointer NULL or not 4-byte aligned");
   return decode_impl(cfg, w, x, B, max_position, positions, kv, ssm_state, conv_state, residual, out, ws,
                      ws_bytes, stream);
+}
+
+int hymba_mixer_paged_workspace_size(const hymba_layer_cfg* cfg, int batch, int top_pages, size_t* bytes) {
+  HY_TRY(check_cfg(cfg));
+  if (bytes == nullptr || batch < 1 || top_pages < 0)
+    return fail(HYMBA_ERR_INVALID_ARG, "bytes NULL, batch %d or top_pages %d", batch, top_pages);
+  *bytes = paged_decode_layout(dims_of(cfg), batch, top_pages).total;
+  return HYMBA_OK;
+}
+
+int hymba_mixer_decode_paged(const hymba_layer_cfg* cfg, const hymba_layer_weights* w, const hymba_bf16* x,
+                             const int* positions, const hymba_paged_kv* kv, const hymba_page_table* table,
+                             int top_pages, float* ssm_state, float* conv_state, const hymba_bf16* residual,
+                             hymba_bf16* out, void* ws, size_t ws_bytes, hymba_stream stream) {
+  HY_TRY(check_cfg(cfg));
+  if (positions == nullptr || !aligned4(positions))
+    return fail(HYMBA_ERR_INVALID_ARG, "positions pointer NULL or not 4-byte aligned");
+  const PagedDecode pd{kv, table, top_pages};
+  HY_TRY(check_paged_decode(pd, cfg));
+  return decode_impl(cfg, w, x, table->batch, 0, positions, nullptr, ssm_state, conv_state, residual, out, ws, ws_bytes,
+                     stream, nullptr, 0.f, nullptr, &pd);
 }
 
 int hymba_gemm_bf16(const hymba_bf16* A, const hymba_bf16* Bm, const hymba_bf16* residual, hymba_bf16* C, int M,

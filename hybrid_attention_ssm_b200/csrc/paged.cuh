@@ -122,6 +122,8 @@ struct PagedAppendParams {
   void *pk, *pv;                    // the pool; pk NULL: only the queries are rotated
   long long page_stride, head_stride, row_stride;
   void *k_lo, *k_hi;                // [n_pages, Hkv, D], or NULL
+  unsigned* clear;                  // n_clear words that the step kernel zeroes (the counters of an
+  int n_clear;                      // attention that follows in the same call), or NULL
   DevStatus* status;
   unsigned long long turns[64];     // theta_j / (2 pi) in units of 2^-64
 };
@@ -330,6 +332,8 @@ __global__ void __launch_bounds__(PAP_STEP_THREADS) paged_append_step_kernel(con
   const long long i = (long long)blockIdx.x * PAP_STEP_THREADS + threadIdx.x;
   const int part = (int)(i % PARTS), g = (int)(i / PARTS % p.Hkv);
   const long long bl = i / PARTS / p.Hkv;
+  if (p.clear != nullptr)
+    for (long long k = i; k < p.n_clear; k += (long long)gridDim.x * PAP_STEP_THREADS) p.clear[k] = 0;
   if (bl >= p.B) return;
   const int b = (int)bl;
   const int pos = p.start[b] + p.start_add;
@@ -693,6 +697,7 @@ struct PagedSelectParams {
   const int* table;
   long long table_stride;
   const int* lens;
+  int len_add;               // added to every length
   int width, B, Hkv, G, n_pages, ps_log2, n_first, n_last, top;
   int* page_idx;             // [B, Hkv, top]
   DevStatus* status;
@@ -701,6 +706,11 @@ struct PagedSelectParams {
 __device__ __forceinline__ int paged_len(int len, int width, int ps_log2) {
   const long long cap = (long long)width << ps_log2;
   return len < 0 ? 0 : (int)min((long long)len, cap);
+}
+
+__device__ __forceinline__ int paged_raw_len(const int* lens, int b, int add) {
+  const int l = lens[b];
+  return l > 0x7fffffff - add ? l : l + add;
 }
 
 constexpr int PSEL_THREADS = 256;
@@ -729,7 +739,7 @@ __global__ void __launch_bounds__(PSEL_THREADS, 2)
 #pragma unroll
   for (int h = 0; h < QB; ++h)
     if (h < p.G) qr[h] = *reinterpret_cast<const uint4*>(q + h * D);
-  const int raw_len = p.lens[b];
+  const int raw_len = paged_raw_len(p.lens, b, p.len_add);
   const int len = paged_len(raw_len, p.width, p.ps_log2);
   if (len != raw_len && tid == 0) report_error(p.status, DEV_ERR_BOUNDS, 621);
   const int n = (int)(((long long)len + (1 << p.ps_log2) - 1) >> p.ps_log2);
@@ -1063,10 +1073,7 @@ __device__ __forceinline__ PaTiles pa_tiles(const PagedAttnParams& p, int raw_le
   if (r.n_tiles < 1) r.n_tiles = 1;                       // an empty sequence: one tile without keys
   return r;
 }
-__device__ __forceinline__ int pa_len(const PagedAttnParams& p, int b) {
-  const int l = p.lens[b];
-  return l > 0x7fffffff - p.len_add ? l : l + p.len_add;
-}
+__device__ __forceinline__ int pa_len(const PagedAttnParams& p, int b) { return paged_raw_len(p.lens, b, p.len_add); }
 __device__ __forceinline__ unsigned long long low_bits(int n) {
   return n <= 0 ? 0ull : (n >= 64 ? ~0ull : (1ull << n) - 1);
 }

@@ -76,6 +76,15 @@ int check_table(const hymba_page_table* t) {
     return fail(HYMBA_ERR_INVALID_ARG, "page table (NULL, misaligned, or sizes)");
   return HYMBA_OK;
 }
+int check_select(const hymba_paged_kv* kv, const hymba_page_table* table, int n_first, int n_last, int top_pages) {
+  if (kv->k_lo == nullptr) return fail(HYMBA_ERR_INVALID_ARG, "page selection needs the cache's page bounds");
+  if (table->width > PAGED_MAX_SELECT_WIDTH)
+    return fail(HYMBA_ERR_UNSUPPORTED, "page selection over %d pages (at most %d)", table->width,
+                PAGED_MAX_SELECT_WIDTH);
+  if (n_first < 0 || n_last < 0 || top_pages < 1 || (long long)n_first + n_last > top_pages)
+    return fail(HYMBA_ERR_INVALID_ARG, "top_pages %d with %d first and %d last", top_pages, n_first, n_last);
+  return HYMBA_OK;
+}
 int check_paged_ws(const void* ws, size_t ws_bytes, size_t need) {
   if (ws == nullptr || (reinterpret_cast<uintptr_t>(ws) & 255u)) return fail(HYMBA_ERR_INVALID_ARG, "workspace");
   if (ws_bytes < need) return fail(HYMBA_ERR_WORKSPACE, "workspace %zu < %zu bytes", ws_bytes, need);
@@ -235,12 +244,148 @@ int launch_paged_attn(const hymba_paged_kv* kv, PagedAttnParams& p, uint8_t* ws,
   });
 }
 
+// Enqueue the selection; p holds everything but the pool's fields.
+int launch_paged_select(const hymba_paged_kv* kv, PagedSelectParams& p, cudaStream_t st) {
+  p.k_lo = kv->k_lo;
+  p.k_hi = kv->k_hi;
+  p.Hkv = kv->n_kv_heads;
+  p.n_pages = kv->n_pages;
+  p.ps_log2 = log2_int(kv->page_size);
+  // the largest cluster that leaves the CTAs of the call resident at once (four per SM) and at
+  // least 64 pages to a CTA
+  const long long lists = (long long)p.B * p.Hkv;
+  int cluster = 8;
+  while (cluster > 1 && (lists * cluster > 4 * 148 || p.width < 64 * cluster)) cluster >>= 1;
+  if (lists * cluster > 0x7fffffff) return fail(HYMBA_ERR_UNSUPPORTED, "batch too large");
+  return paged_dispatch(kv, [&](auto e, auto d) {
+    auto kern = paged_select_kernel<decltype(e), decltype(d)::value>;
+    static bool attr[64] = {false};
+    int dcur = 0;
+    HY_CUDA(cudaGetDevice(&dcur));
+    if (!attr[dcur & 63]) {
+      HY_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, PAGED_MAX_SELECT_WIDTH * 8));
+      attr[dcur & 63] = true;
+    }
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)(lists * cluster));
+    cfg.blockDim = dim3(PSEL_THREADS);
+    cfg.dynamicSmemBytes = (size_t)p.width * 8;
+    cfg.stream = st;
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = cluster;
+    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 2;
+    prof_begin("paged_select", cfg.stream);
+    HY_CUDA(cudaLaunchKernelEx(&cfg, kern, p, cluster));
+    prof_end(cfg.stream);
+    return (int)HYMBA_OK;
+  });
+}
+
 int paged_group(const hymba_paged_kv* kv, int n_q_heads, int* group) {
   if (n_q_heads < 1 || n_q_heads % kv->n_kv_heads || n_q_heads / kv->n_kv_heads > 16)
     return fail(HYMBA_ERR_UNSUPPORTED, "%d query heads over %d KV heads (1 to 16 per KV head)", n_q_heads,
                 kv->n_kv_heads);
   *group = n_q_heads / kv->n_kv_heads;
   return HYMBA_OK;
+}
+
+// ---- a mixer's decode step over a paged cache -------------------------------------------
+struct PagedDecode {
+  const hymba_paged_kv* kv;
+  const hymba_page_table* table;
+  int top_pages;   // 0: every page
+};
+// Workspace after the decode step's own buffers (laid out as for one key: no key splits).
+struct PagedDecodeWs {
+  size_t q, arrived, part, idx, total;
+};
+DecodeWs paged_decode_base(const Dims& m, int B) { return decode_layout(m, B, true, 1); }
+PagedDecodeWs paged_decode_layout(const Dims& m, int B, int top_pages) {
+  PagedDecodeWs w;
+  size_t off = paged_decode_base(m, B).total;
+  auto take = [&](size_t bytes) { size_t o = off; off = align256(off + bytes); return o; };
+  w.q = take((size_t)B * m.qw * 2);
+  w.arrived = take((size_t)PA_MAX_GRID * sizeof(unsigned));
+  w.part = take((size_t)PA_MAX_GRID * 2 * (m.Hq / m.Hkv) * (m.D + 4) * 4);
+  w.idx = take((size_t)B * m.Hkv * top_pages * 4);
+  w.total = off;
+  return w;
+}
+// first pages to select whatever their scores: those of the meta tokens
+int paged_meta_pages(const hymba_paged_kv* kv, int n_meta) { return cdiv(n_meta, kv->page_size); }
+
+int check_paged_decode(const PagedDecode& d, const hymba_layer_cfg* cfg) {
+  HY_TRY(check_paged(d.kv, true));
+  HY_TRY(check_table(d.table));
+  if (d.kv->n_kv_heads != cfg->n_kv_heads || d.kv->head_dim != cfg->head_dim)
+    return fail(HYMBA_ERR_INVALID_ARG, "paged cache of %d heads x %d for a layer of %d x %d", d.kv->n_kv_heads,
+                d.kv->head_dim, cfg->n_kv_heads, cfg->head_dim);
+  if (d.top_pages < 0 || (d.top_pages > 0 && !cfg->is_global))
+    return fail(HYMBA_ERR_INVALID_ARG, "top_pages %d (page selection is for global layers)", d.top_pages);
+  if (d.top_pages > 0) HY_TRY(check_select(d.kv, d.table, paged_meta_pages(d.kv, cfg->n_meta), 1, d.top_pages));
+  return HYMBA_OK;
+}
+
+// RoPE and append of the new tokens from in_proj's split-K slices, the page selection, and the
+// attention into o [B, Hq*D] fp32, on `st`.  The append clears the attention's counters: the
+// workspace serves other calls in between.
+int launch_paged_decode(const PagedDecode& d, const hymba_layer_cfg* cfg, const Dims& m, int B, const int* positions,
+                        const float* proj, int n_slices, bool own_kv, const PagedDecodeWs& L, uint8_t* ws, float* o,
+                        const DeviceInfo& dev, cudaStream_t st) {
+  const hymba_page_table* t = d.table;
+  DevStatus* status = reinterpret_cast<DevStatus*>(ws);
+  PagedAppendParams ap{};
+  ap.q = proj;
+  ap.k = own_kv ? proj + m.qw : nullptr;
+  ap.v = own_kv ? proj + m.qw + m.kvw : nullptr;
+  ap.q_stride = ap.k_stride = ap.v_stride = m.P;
+  ap.src = PDT_F32;
+  ap.n_slices = n_slices;
+  ap.slice_stride = (long long)B * m.P;
+  ap.q_out = ws + L.q;
+  ap.start = positions;
+  ap.table = t->pages; ap.table_stride = t->stride; ap.width = t->width;
+  ap.B = ap.T = B;
+  ap.G = m.Hq / m.Hkv;
+  ap.clear = reinterpret_cast<unsigned*>(ws + L.arrived);
+  ap.n_clear = PA_MAX_GRID;
+  ap.status = status;
+  HY_TRY(launch_paged_append(d.kv, ap, cfg->rope_base, dev.sms, st));
+  if (d.top_pages > 0) {
+    PagedSelectParams sp{};
+    sp.q = ws + L.q; sp.q_stride = m.qw;
+    sp.table = t->pages; sp.table_stride = t->stride; sp.width = t->width;
+    sp.lens = positions;
+    sp.len_add = 1;
+    sp.B = B; sp.G = ap.G;
+    sp.n_first = paged_meta_pages(d.kv, m.M); sp.n_last = 1; sp.top = d.top_pages;
+    sp.page_idx = reinterpret_cast<int*>(ws + L.idx);
+    sp.status = status;
+    HY_TRY(launch_paged_select(d.kv, sp, st));
+  }
+  PagedAttnParams p{};
+  p.q = ws + L.q; p.q_stride = m.qw;
+  p.out = o; p.out_dt = PDT_F32; p.out_stride = m.qw;
+  p.table = t->pages; p.table_stride = t->stride; p.width = t->width;
+  p.lens = positions;
+  p.len_add = 1;
+  p.page_idx = d.top_pages > 0 ? reinterpret_cast<const int*>(ws + L.idx) : nullptr;
+  p.top = d.top_pages;
+  p.B = B; p.Hq = m.Hq; p.G = ap.G;
+  p.M = cfg->is_global ? 0 : m.M;
+  p.W = cfg->is_global ? 0 : m.W;
+  p.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)m.D));
+  p.status = status;
+  PagedWs aw;
+  aw.arrived = L.arrived;
+  aw.part = L.part;
+  aw.total = L.total;
+  return launch_paged_attn(d.kv, p, ws, aw, dev.sms, st);
 }
 
 }  // namespace
@@ -308,61 +453,22 @@ int hymba_paged_select(const hymba_paged_kv* kv, const hymba_page_table* table, 
   HY_TRY(check_table(table));
   int G = 0;
   HY_TRY(paged_group(kv, n_q_heads, &G));
-  if (kv->k_lo == nullptr) return fail(HYMBA_ERR_INVALID_ARG, "page selection needs the cache's page bounds");
-  if (table->width > PAGED_MAX_SELECT_WIDTH)
-    return fail(HYMBA_ERR_UNSUPPORTED, "page selection over %d pages (at most %d)", table->width,
-                PAGED_MAX_SELECT_WIDTH);
+  HY_TRY(check_select(kv, table, n_first, n_last, top_pages));
   if (seq_lens == nullptr || !aligned4(seq_lens) || page_idx == nullptr || !aligned4(page_idx) || q == nullptr ||
       !aligned16(q) || q_stride < (long long)n_q_heads * kv->head_dim || q_stride % 8)
     return fail(HYMBA_ERR_INVALID_ARG, "seq_lens / page_idx / q");
-  if (n_first < 0 || n_last < 0 || top_pages < 1 || (long long)n_first + n_last > top_pages)
-    return fail(HYMBA_ERR_INVALID_ARG, "top_pages %d with %d first and %d last", top_pages, n_first, n_last);
   HY_TRY(check_paged_ws(ws, ws_bytes, 256));
   DeviceInfo* dev = nullptr;
   HY_TRY(device_info(&dev));
   PagedSelectParams p{};
-  p.k_lo = kv->k_lo; p.k_hi = kv->k_hi;
   p.q = q; p.q_stride = q_stride;
   p.table = table->pages; p.table_stride = table->stride; p.width = table->width;
   p.lens = seq_lens;
-  p.B = table->batch; p.Hkv = kv->n_kv_heads; p.G = G; p.n_pages = kv->n_pages;
-  p.ps_log2 = log2_int(kv->page_size);
+  p.B = table->batch; p.G = G;
   p.n_first = n_first; p.n_last = n_last; p.top = top_pages;
   p.page_idx = page_idx;
   p.status = reinterpret_cast<DevStatus*>(ws);
-  // the largest cluster that leaves the CTAs of the call resident at once (four per SM) and at
-  // least 64 pages to a CTA
-  const long long lists = (long long)p.B * p.Hkv;
-  int cluster = 8;
-  while (cluster > 1 && (lists * cluster > 4 * 148 || p.width < 64 * cluster)) cluster >>= 1;
-  if (lists * cluster > 0x7fffffff) return fail(HYMBA_ERR_UNSUPPORTED, "batch too large");
-  return paged_dispatch(kv, [&](auto e, auto d) {
-    auto kern = paged_select_kernel<decltype(e), decltype(d)::value>;
-    static bool attr[64] = {false};
-    int dcur = 0;
-    HY_CUDA(cudaGetDevice(&dcur));
-    if (!attr[dcur & 63]) {
-      HY_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, PAGED_MAX_SELECT_WIDTH * 8));
-      attr[dcur & 63] = true;
-    }
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)(lists * cluster));
-    cfg.blockDim = dim3(PSEL_THREADS);
-    cfg.dynamicSmemBytes = (size_t)p.width * 8;
-    cfg.stream = (cudaStream_t)stream;
-    cudaLaunchAttribute at[2];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    at[1].id = cudaLaunchAttributeClusterDimension;
-    at[1].val.clusterDim.x = cluster;
-    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 2;
-    prof_begin("paged_select", cfg.stream);
-    HY_CUDA(cudaLaunchKernelEx(&cfg, kern, p, cluster));
-    prof_end(cfg.stream);
-    return (int)HYMBA_OK;
-  });
+  return launch_paged_select(kv, p, (cudaStream_t)stream);
 }
 
 int hymba_paged_attention(const hymba_paged_kv* kv, const hymba_page_table* table, const int* seq_lens, const void* q,

@@ -150,6 +150,11 @@ def lib():
             "hymba_paged_attention": ([ctypes.POINTER(PagedKV), ctypes.POINTER(PageTable), _vp, _vp,
                                        ctypes.c_longlong, _c_int, ctypes.c_float, _c_int, _c_int, _vp, _c_int, _vp,
                                        _c_int, ctypes.c_longlong, _vp, _vp, _c_size, _vp], _c_int),
+            "hymba_mixer_paged_workspace_size": ([ctypes.POINTER(LayerCfg), _c_int, _c_int, ctypes.POINTER(_c_size)],
+                                                 _c_int),
+            "hymba_mixer_decode_paged": ([ctypes.POINTER(LayerCfg), ctypes.POINTER(LayerWeights), _vp, _vp,
+                                          ctypes.POINTER(PagedKV), ctypes.POINTER(PageTable), _c_int, _vp, _vp, _vp,
+                                          _vp, _vp, _c_size, _vp], _c_int),
             "hymba_set_wait_limit_ns": ([ctypes.c_ulonglong], _c_int),
             "hymba_prepend_meta": ([_vp, _vp, _c_int, _c_int, _c_int, _c_int, _vp, _vp], _c_int),
             "hymba_selftest_wait_timeout": ([_vp, _c_size, _vp], _c_int),
@@ -557,6 +562,28 @@ def mixer_decode_ragged(dims, dw: DeviceWeights, x, positions, max_position, kv:
     check(lib().hymba_mixer_decode_ragged(ctypes.byref(cfg), ctypes.byref(dw.c), ptr(x), x.shape[0], ptr(positions),
                                           max_position, ctypes.byref(kv.c), ptr(ssm_state), ptr(conv_state),
                                           ptr(residual), ptr(out), ptr(ws), ws.numel(), stream_handle(stream)))
+
+
+def mixer_paged_workspace_size(dims, batch, top_pages=0) -> int:
+    n = ctypes.c_size_t()
+    cfg = make_cfg(dims)
+    check(lib().hymba_mixer_paged_workspace_size(ctypes.byref(cfg), batch, top_pages, ctypes.byref(n)))
+    return n.value
+
+
+def mixer_decode_paged(dims, dw: DeviceWeights, x, positions, cache: PagedCache, table, ssm_state, conv_state, out, ws,
+                       top_pages=0, residual=None, stream=None, cfg=None):
+    """hymba_mixer_decode over a paged cache: positions [B] int32, table [B, width] int32;
+    top_pages > 0 (global layers): attention over that many selected pages."""
+    st = _paged_stream(cache, stream, x, positions, table, ssm_state, conv_state, out, ws, residual)
+    cfg = make_cfg(dims) if cfg is None else cfg
+    tb, B = _page_table(table)
+    if x.shape != (B, dims.d_model) or out.shape != x.shape or not (x.is_contiguous() and out.is_contiguous()):
+        _refuse("x and out must be contiguous [batch, d_model]")
+    check(lib().hymba_mixer_decode_paged(ctypes.byref(cfg), ctypes.byref(dw.c), ptr(x),
+                                         _int32_vector(positions, B, "positions"), cache.ref, ctypes.byref(tb),
+                                         top_pages, ptr(ssm_state), ptr(conv_state), ptr(residual), ptr(out), ptr(ws),
+                                         ws.numel(), st))
 
 
 def mixer_decode_noalloc(dims, dw: DeviceWeights, x, position, kv: Cache, ssm_state, conv_state, out,

@@ -410,6 +410,25 @@ int hymba_paged_attention(const hymba_paged_kv* kv, const hymba_page_table* tabl
                           int top_pages, void* out, int out_dtype, long long out_stride, float* lse, void* workspace,
                           size_t ws_bytes, hymba_stream stream);
 
+/* hymba_mixer_decode over a paged cache: sequence b's new token (x [batch, d]) is at
+ * positions[b] (device, int32 [table->batch], meta tokens counted, >= 0), its page already in
+ * the block table.  own/producer layers append its key and value; then the layer attends over
+ * the sequence's pages: a global layer over all of them, or with top_pages > 0 over the
+ * top_pages that hymba_paged_select chooses (the meta tokens' pages and the last one among
+ * them; needs page bounds), an SWA layer over the meta tokens and its window (pages behind the
+ * window that hold no meta token are not read and may have been given back).  A consumer
+ * layer reads the pages its producer's step has appended to.  The pool may be F16 (the
+ * contiguous caches' type) or BF16.  States, residual and out as hymba_mixer_decode.
+ * The calls of a step make the same sums as hymba_mixer_decode_ragged in another order.
+ * Prefill writes contiguous caches; hymba_paged_append with rope_base 0 moves their rows into
+ * pages.  Workspace: hymba_mixer_paged_workspace_size; its status word also records what
+ * hymba_paged_append and hymba_paged_attention record. */
+int hymba_mixer_paged_workspace_size(const hymba_layer_cfg* cfg, int batch, int top_pages, size_t* bytes);
+int hymba_mixer_decode_paged(const hymba_layer_cfg* cfg, const hymba_layer_weights* w, const hymba_bf16* x,
+                             const int* positions, const hymba_paged_kv* kv, const hymba_page_table* table,
+                             int top_pages, float* ssm_state, float* conv_state, const hymba_bf16* residual,
+                             hymba_bf16* out, void* workspace, size_t ws_bytes, hymba_stream stream);
+
 /* Byte offsets, inside a prefill workspace, of the stage buffers of the last prefill (for
  * stage-by-stage checks).  Layouts (rows r = b*T + t):
  *   q      [B*T, Hq*D]  fp16  queries after RoPE
