@@ -698,14 +698,15 @@ struct PagedSelectParams {
   long long table_stride;
   const int* lens;
   int len_add;               // added to every length
-  int width, B, Hkv, G, n_pages, ps_log2, n_first, n_last, top;
+  int width, cap, B, Hkv, G, n_pages, ps_log2, n_first, n_last, top;
   int* page_idx;             // [B, Hkv, top]
   DevStatus* status;
 };
 
-__device__ __forceinline__ int paged_len(int len, int width, int ps_log2) {
-  const long long cap = (long long)width << ps_log2;
-  return len < 0 ? 0 : (int)min((long long)len, cap);
+// Sequence lengths: lens[b] + add, clamped to 0 .. cap, the positions that the table holds.
+__device__ __forceinline__ int paged_len(int len, int cap) { return max(0, min(len, cap)); }
+__device__ __forceinline__ int paged_pages(int len, int ps_log2) {
+  return (int)(((unsigned)len + (1u << ps_log2) - 1u) >> ps_log2);
 }
 
 __device__ __forceinline__ int paged_raw_len(const int* lens, int b, int add) {
@@ -740,9 +741,9 @@ __global__ void __launch_bounds__(PSEL_THREADS, 2)
   for (int h = 0; h < QB; ++h)
     if (h < p.G) qr[h] = *reinterpret_cast<const uint4*>(q + h * D);
   const int raw_len = paged_raw_len(p.lens, b, p.len_add);
-  const int len = paged_len(raw_len, p.width, p.ps_log2);
+  const int len = paged_len(raw_len, p.cap);
   if (len != raw_len && tid == 0) report_error(p.status, DEV_ERR_BOUNDS, 621);
-  const int n = (int)(((long long)len + (1 << p.ps_log2) - 1) >> p.ps_log2);
+  const int n = paged_pages(len, p.ps_log2);
   int* out = p.page_idx + (long long)bg * p.top;
   if (n <= p.top) {   // every page (the whole cluster takes this branch)
     if (rank == 0)
@@ -1040,7 +1041,7 @@ struct PagedAttnParams {
   const int* lens;
   int len_add;                // added to every length
   const int* page_idx;        // [B, Hkv, top] page numbers within the sequence, or NULL
-  int top, width, B, Hq, Hkv, G, n_pages, ps_log2, M, W;
+  int top, width, cap, B, Hq, Hkv, G, n_pages, ps_log2, M, W;
   int dim_row, dim_head;      // tensor-map dimensions (1..3) of rows and heads; pages have the other
   float scale_log2;
   float* part;                // [grid][2][G][D + 4]: slot 1 the item that begins in the CTA
@@ -1056,14 +1057,14 @@ struct PaTiles {
 };
 __device__ __forceinline__ PaTiles pa_tiles(const PagedAttnParams& p, int raw_len) {
   PaTiles r;
-  r.len = paged_len(raw_len, p.width, p.ps_log2);
-  const int all = (int)(((long long)r.len + PA_KT - 1) / PA_KT);
+  r.len = paged_len(raw_len, p.cap);
+  const int all = (int)(((unsigned)r.len + PA_KT - 1) / PA_KT);
   r.head = all;
   r.skip = 0;
   r.n_tiles = all;
   if (p.page_idx != nullptr) {
-    const int pages = (int)(((long long)r.len + (1 << p.ps_log2) - 1) >> p.ps_log2);
-    r.n_tiles = (int)((((long long)min(pages, p.top) << p.ps_log2) + PA_KT - 1) / PA_KT);
+    const unsigned rows = (unsigned)min(paged_pages(r.len, p.ps_log2), p.top) << p.ps_log2;   // at most 2^31
+    r.n_tiles = (int)((rows + PA_KT - 1) / PA_KT);
   } else if (p.W > 0) {
     const int w0 = max(0, r.len - p.W) / PA_KT;           // the window's first tile
     r.head = min(w0, (p.M + PA_KT - 1) / PA_KT);
@@ -1147,21 +1148,16 @@ __device__ __forceinline__ bool pa_arrive(const PagedAttnParams& p, int c0, int 
 }
 // After a wait that gave up, the counts are completed all the same, so that the next call on
 // the workspace finds them at zero: count this CTA's parts of cut items that it has not counted
-// (done: bit 0 an item begun earlier, bit 1 one that goes on), walking its share by items.
-__device__ __noinline__ void pa_arrive_rest(const PagedAttnParams& p, int b, int g, int t, int t0, int t1,
-                                            const PaShares& sh, int done) {
-  for (int cur = t0; cur < t1;) {
+// (done: bit 0 an item begun earlier, bit 1 one that goes on), walking the items.
+__device__ __noinline__ void pa_arrive_rest(const PagedAttnParams& p, int t0, int t1, const PaShares& sh, int done) {
+  int beg = 0;
+  for (int b = 0; b < p.B && beg < t1; ++b) {
     const int nt = pa_tiles(p, pa_len(p, b)).n_tiles;
-    const int beg = cur - t, end = beg + nt, stop = min(end, t1);
-    if ((beg < t0 || end > t1) && !(done & (beg < t0 ? 1 : 2))) {
+    for (int g = 0; g < p.Hkv && beg < t1; ++g, beg += nt) {
+      const int end = beg + nt;
+      if (end <= t0 || (beg >= t0 && end <= t1) || (done & (beg < t0 ? 1 : 2))) continue;
       const int c0 = sh.owner(beg);
       pa_arrive(p, c0, sh.owner(end - 1) - c0 + 1);
-    }
-    cur = stop;
-    t = 0;
-    if (++g == p.Hkv) {
-      g = 0;
-      b = min(b + 1, p.B - 1);
     }
   }
 }
@@ -1182,11 +1178,21 @@ __device__ __forceinline__ bool pa_join(const PagedAttnParams& p, int item, int 
     a.clear();
     if (hs < heads && h0 + hs < p.G) {
       const float* src = p.part + (((long long)c0 * 2) * p.G + h0 + hs) * LD;
-#pragma unroll 8
-      for (int i = s0; i < parts; i += per_head) {
-        const float* row = src + ((long long)i * 2 + (i == 0 ? 1 : 0)) * p.G * LD;
-        const float2 ml = __ldcg(reinterpret_cast<const float2*>(row + D));
-        a.add(ml.x, ml.y, __ldcg(reinterpret_cast<const float4*>(row) + quad));
+      constexpr int UN = 8;   // parts whose loads are in flight together
+#pragma unroll 1
+      for (int i0 = s0; i0 < parts; i0 += UN * per_head) {
+        float2 ml[UN];
+        float4 x[UN];
+#pragma unroll
+        for (int u = 0; u < UN; ++u) {
+          const int i = min(i0 + u * per_head, parts - 1);   // (past the end: the last one, not added)
+          const float* row = src + ((long long)i * 2 + (i == 0 ? 1 : 0)) * p.G * LD;
+          ml[u] = __ldcg(reinterpret_cast<const float2*>(row + D));
+          x[u] = __ldcg(reinterpret_cast<const float4*>(row) + quad);
+        }
+#pragma unroll
+        for (int u = 0; u < UN; ++u)
+          if (i0 + u * per_head < parts) a.add(ml[u].x, ml[u].y, x[u]);
       }
     }
     float* row = sh + sub * LD;
@@ -1229,8 +1235,7 @@ __global__ void __launch_bounds__(PaShape<D, NHB>::THREADS, 1)
     return prows[k][slot][hh];
   };
   __shared__ PaPart pinfo[GROUPS][2];
-  __shared__ int wsum[NWARPS];
-  __shared__ int start[GROUPS][3];                   // the sequence, kv head and tile that a group starts at
+  __shared__ int wsum[NWARPS];                       // tiles of a warp's sequences
   __shared__ int counted, abort_flag;                // parts counted so far (bits as pa_arrive_rest)
   __shared__ PaPart joins[2];                        // the cut items that this CTA joins
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -1269,41 +1274,28 @@ __global__ void __launch_bounds__(PaShape<D, NHB>::THREADS, 1)
     const int up = __shfl_up_sync(0xffffffffu, inc, o);
     if (lane >= o) inc += up;
   }
+  // tiles up to and with a thread's sequences, in its warp: a copy for each producer warp, where
+  // its ring will be
+#pragma unroll
+  for (int k = 0; k < GROUPS; ++k) reinterpret_cast<int*>(rings + k * STAGES * S::STAGE)[tid] = inc;
+  fence_proxy_async_smem();
   if (lane == 31) wsum[warp] = inc;
   __syncthreads();
-  int before = inc - mine, total = 0;
+  int wins = lane < NWARPS ? wsum[lane] : 0;   // tiles up to and with warp `lane`'s sequences
 #pragma unroll
-  for (int w = 0; w < NWARPS; ++w) {
-    if (w < warp) before += wsum[w];
-    total += wsum[w];
+  for (int o = 1; o < 16; o <<= 1) {
+    const int up = __shfl_up_sync(0xffffffffu, wins, o);
+    if (lane >= o) wins += up;
   }
+  const int total = __shfl_sync(0xffffffffu, wins, NWARPS - 1);
   const int n_cta = min((int)gridDim.x, total);
   if ((int)blockIdx.x >= n_cta) return;
   const PaShares shares(total, n_cta);
   const int t0 = shares.begin(blockIdx.x), t1 = shares.begin(blockIdx.x + 1);
-  const int gq0 = (t1 - t0) / GROUPS, gr0 = (t1 - t0) % GROUPS;
-  auto share = [&](int k) { return t0 + k * gq0 + min(k, gr0); };   // of group k: share(k) .. share(k + 1)
-  if (mine > 0) {
-#pragma unroll
-    for (int k = 0; k < GROUPS; ++k) {
-      int left = share(k) - before;
-      if (left < 0 || left >= mine) continue;
-      for (int i = b0; i < b1; ++i) {
-        const int nt = pa_tiles(p, pa_len(p, i)).n_tiles;
-        if (left < nt * p.Hkv || i + 1 == b1) {
-          start[k][0] = i;
-          start[k][1] = left / nt;
-          start[k][2] = left % nt;
-          break;
-        }
-        left -= nt * p.Hkv;
-      }
-    }
-  }
-  __syncthreads();
   const bool producer = warp >= CWARPS;
   const int grp = producer ? warp - CWARPS : warp / 4;
-  const int u0 = share(grp), u1 = share(grp + 1), n_mine = u1 - u0;
+  const int gq0 = (t1 - t0) / GROUPS, gr0 = (t1 - t0) % GROUPS;
+  const int u0 = t0 + grp * gq0 + min(grp, gr0), n_mine = gq0 + (grp < gr0 ? 1 : 0), u1 = u0 + n_mine;
   uint64_t* full = full_bars[grp];
   uint64_t* empty = empty_bars[grp];
   uint8_t* ring = rings + grp * STAGES * S::STAGE;
@@ -1313,8 +1305,28 @@ __global__ void __launch_bounds__(PaShape<D, NHB>::THREADS, 1)
     if (n_mine == 0) return;
     const int ps = 1 << p.ps_log2;
     const int R = min(ps, PA_KT), n_chunk = PA_KT / R;    // a tile's page pieces
-    int b = start[grp][0], g = start[grp][1], t = start[grp][2];
+    // the sequence, kv head and tile that the group starts at: the warp, the thread and the
+    // sequence that hold tile u0
+    int b, g, t, left = u0;
+    {
+      const int* upto = reinterpret_cast<const int*>(ring);
+      const int w = __ffs(__ballot_sync(0xffffffffu, wins > left)) - 1;
+      const int skip = __shfl_sync(0xffffffffu, wins, max(w - 1, 0));
+      if (w > 0) left -= skip;
+      const unsigned hit = __ballot_sync(0xffffffffu, upto[w * 32 + lane] > left);
+      const int owner = w * 32 + __ffs(hit) - 1;
+      if (owner > w * 32) left -= upto[owner - 1];
+      b = owner * per;
+      __syncwarp();
+      fence_proxy_async_smem();   // from here on the ring belongs to the copies
+    }
     PaTiles sq = pa_tiles(p, pa_len(p, b));
+    while (left >= sq.n_tiles * p.Hkv && b + 1 < p.B) {
+      left -= sq.n_tiles * p.Hkv;
+      sq = pa_tiles(p, pa_len(p, ++b));
+    }
+    g = left / sq.n_tiles;
+    t = left - g * sq.n_tiles;
     int next_len = b + 1 < p.B ? pa_len(p, b + 1) : 0;
     bool ok = true;
     // One tile's page piece of this lane: the table's page (checked when it is used, so that the
@@ -1335,7 +1347,7 @@ __global__ void __launch_bounds__(PaShape<D, NHB>::THREADS, 1)
         bool in = true;
         if (p.page_idx != nullptr) {
           const int e = key >> p.ps_log2;
-          const int pages = (int)(((long long)sq.len + ps - 1) >> p.ps_log2);
+          const int pages = paged_pages(sq.len, p.ps_log2);
           logical = e < min(pages, p.top) ? p.page_idx[((long long)b * p.Hkv + g) * p.top + e] : -1;
           in = logical >= 0 && logical < pages;
           pos = in ? (logical << p.ps_log2) + (key & (ps - 1)) : 0;
@@ -1702,13 +1714,14 @@ __global__ void __launch_bounds__(PaShape<D, NHB>::THREADS, 1)
       }
       if (ok) ok = fin_sync();
     }
-    // (every load of the rings has landed and been read: they are scratch now)
-    for (int s = 0; s < 2 && ok; ++s)
-      if (joins[s].item >= 0)
-        ok = pa_join<D, CWARPS>(p, joins[s].item, joins[s].c0, joins[s].parts, tid, reinterpret_cast<float*>(rings),
-                                fin_sync);
+    // (the groups' parts have been merged and published: their merge rows are scratch now)
+#pragma unroll 1
+    for (int s = 0; s < 2 && ok; ++s) {
+      const PaPart j = joins[s];
+      if (j.item >= 0) ok = pa_join<D, CWARPS>(p, j.item, j.c0, j.parts, tid, &mos[0][0][0][0], fin_sync);
+    }
   }
-  if (!ok && tid == 0) pa_arrive_rest(p, start[0][0], start[0][1], start[0][2], t0, t1, shares, counted);
+  if (!ok && tid == 0) pa_arrive_rest(p, t0, t1, shares, counted);
 }
 
 }  // namespace hymba

@@ -91,6 +91,10 @@ int check_paged_ws(const void* ws, size_t ws_bytes, size_t need) {
   return HYMBA_OK;
 }
 inline bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+// positions that a table row can name, at most 2^31 - 1
+inline int paged_cap(int width, int page_size) {
+  return (int)std::min<long long>((long long)width * page_size, 0x7fffffff);
+}
 inline int log2_int(int v) {
   int l = 0;
   while ((1 << l) < v) ++l;
@@ -219,6 +223,7 @@ int launch_paged_attn(const hymba_paged_kv* kv, PagedAttnParams& p, uint8_t* ws,
   p.Hkv = kv->n_kv_heads;
   p.n_pages = kv->n_pages;
   p.ps_log2 = log2_int(kv->page_size);
+  p.cap = paged_cap(p.width, kv->page_size);
   p.arrived = reinterpret_cast<unsigned*>(ws + L.arrived);
   p.part = reinterpret_cast<float*>(ws + L.part);
   // tiles are counted in 32 bits (2^31 of them are 16 TB of keys of one head)
@@ -251,6 +256,7 @@ int launch_paged_select(const hymba_paged_kv* kv, PagedSelectParams& p, cudaStre
   p.Hkv = kv->n_kv_heads;
   p.n_pages = kv->n_pages;
   p.ps_log2 = log2_int(kv->page_size);
+  p.cap = paged_cap(p.width, kv->page_size);
   // the largest cluster that leaves the CTAs of the call resident at once (four per SM) and at
   // least 64 pages to a CTA
   const long long lists = (long long)p.B * p.Hkv;

@@ -291,7 +291,7 @@ def _refuse(msg):
     raise HymbaError(ERR_INVALID_ARG, msg)
 
 
-def _paged_stream(cache, stream, *tensors):
+def _paged_stream(cache, stream, tensors):
     """The stream to launch on, after checking that every tensor lives on the cache's device and
     that this is the device the library will launch on."""
     dev = cache.device
@@ -307,7 +307,7 @@ def _paged_stream(cache, stream, *tensors):
 
 def _page_table(table):
     st = table.stride()
-    if table.dim() != 2 or table.dtype != torch.int32 or st[1] != 1:
+    if len(st) != 2 or st[1] != 1 or table.dtype is not torch.int32:
         _refuse("block table must be int32 [batch, width] with contiguous rows")
     B, width = table.shape
     # (a single row's stride is whatever torch made it)
@@ -315,24 +315,32 @@ def _page_table(table):
 
 
 def _int32_vector(t, n, name):
-    if t.dtype != torch.int32 or t.shape != (n,) or not t.is_contiguous():
+    if t.dtype is not torch.int32 or t.shape != (n,) or not t.is_contiguous():
         _refuse(f"{name} must be a contiguous int32 vector of {n}")
     return t.data_ptr()
 
 
-def _head_rows(t, D, name):
+def _head_rows(t, shape, name):
     """Row stride of [rows, heads, D] whose heads are contiguous."""
-    sh, st = t.shape, t.stride()
-    if len(sh) != 3 or sh[2] != D or st[2] != 1 or (st[1] != D and sh[1] != 1):
-        _refuse(f"{name} must be [rows, heads, {D}] with contiguous heads")
-    return sh[1] * D if sh[0] <= 1 else st[0]
+    st = t.stride()
+    if t.shape != shape or st[2] != 1 or (st[1] != shape[2] and shape[1] != 1):
+        _refuse(f"{name} must be {tuple(shape)} with contiguous heads, got {tuple(t.shape)}")
+    return shape[1] * shape[2] if shape[0] <= 1 else st[0]
+
+
+def _query_shape(cache, q, B):
+    shape = q.shape
+    if len(shape) != 3 or shape[0] != B or shape[2] != cache.head_dim or q.dtype is not cache.dtype:
+        _refuse("q must be [batch, Hq, D] in the pool's type")
+    return shape
 
 
 def _page_list(page_idx, cache, B):
-    if not (page_idx.dtype == torch.int32 and page_idx.dim() == 3 and page_idx.is_contiguous() and
-            page_idx.shape[:2] == (B, cache.n_kv_heads)):
+    shape = page_idx.shape
+    if (page_idx.dtype is not torch.int32 or len(shape) != 3 or shape[0] != B or shape[1] != cache.n_kv_heads or
+            not page_idx.is_contiguous()):
         _refuse("page_idx must be contiguous int32 [batch, Hkv, top_pages]")
-    return page_idx.data_ptr(), page_idx.shape[2]
+    return page_idx.data_ptr(), shape[2]
 
 
 def paged_workspace_size(cache: PagedCache, batch, n_q_heads, max_pages) -> int:
@@ -351,7 +359,7 @@ def paged_append(cache: PagedCache, table, start, k, v, ws, q=None, q_out=None, 
     token per sequence).  k and v may be None together.  rope_base 0: no rotation."""
     if (k is None) != (v is None) or (q is None) != (q_out is None) or (k is None and q is None):
         _refuse("paged_append: k and v go together, q and q_out go together")
-    st = _paged_stream(cache, stream, table, start, k, v, ws, q, q_out, cu_new)
+    st = _paged_stream(cache, stream, (table, start, k, v, ws, q, q_out, cu_new))
     tb, B = _page_table(table)
     D = cache.head_dim
     src = k if k is not None else q
@@ -359,17 +367,17 @@ def paged_append(cache: PagedCache, table, start, k, v, ws, q=None, q_out=None, 
     kp = vp = qp = qo = None
     ks = vs = qs = Hq = 0
     if k is not None:
-        want = (T, cache.n_kv_heads, D)
-        if k.shape != want or v.shape != want or v.dtype != dt:
-            _refuse(f"paged_append: k {tuple(k.shape)} {k.dtype}, v {tuple(v.shape)} {v.dtype}")
-        kp, vp, ks, vs = k.data_ptr(), v.data_ptr(), _head_rows(k, D, "k"), _head_rows(v, D, "v")
+        shape = (T, cache.n_kv_heads, D)
+        kp, vp, ks, vs = k.data_ptr(), v.data_ptr(), _head_rows(k, shape, "k"), _head_rows(v, shape, "v")
+        if v.dtype is not dt:
+            _refuse(f"paged_append: k {dt}, v {v.dtype}")
     if q is not None:
-        qs, Hq = _head_rows(q, D, "q"), q.shape[1]
-        if q.shape[0] != T or q.dtype != dt:
-            _refuse(f"paged_append: q {tuple(q.shape)} {q.dtype}")
-        if q_out.shape != q.shape or q_out.dtype != cache.dtype or not q_out.is_contiguous():
+        shape = q.shape
+        if len(shape) != 3 or shape[0] != T or shape[2] != D or q.dtype is not dt:
+            _refuse(f"paged_append: q {tuple(shape)} {q.dtype}")
+        if q_out.shape != shape or q_out.dtype is not cache.dtype or not q_out.is_contiguous():
             _refuse("paged_append: q_out must be contiguous, shaped like q, in the pool's type")
-        qp, qo = q.data_ptr(), q_out.data_ptr()
+        qs, Hq, qp, qo = _head_rows(q, shape, "q"), shape[1], q.data_ptr(), q_out.data_ptr()
     rc = lib().hymba_paged_append(cache.ref, ctypes.byref(tb), _int32_vector(start, B, "start"),
                                   None if cu_new is None else _int32_vector(cu_new, B + 1, "cu_new"), T,
                                   _DT_CODE.get(dt, -1), kp, ks, vp, vs, qp, qs, Hq, qo, rope_base, ws.data_ptr(),
@@ -382,14 +390,13 @@ def paged_select(cache: PagedCache, q, table, seq_lens, page_idx, ws, n_first=1,
     """hymba_paged_select: page_idx [B, Hkv, top] int32 receives, per sequence and KV head, the
     pages (numbers within the sequence, ascending, -1 behind the last) that the rotated query
     q [B, Hq, D] should read: the first n_first, the last n_last and the best by page bounds."""
-    st = _paged_stream(cache, stream, q, table, seq_lens, page_idx, ws)
+    st = _paged_stream(cache, stream, (q, table, seq_lens, page_idx, ws))
     tb, B = _page_table(table)
-    qs = _head_rows(q, cache.head_dim, "q")
-    if q.shape[0] != B or q.dtype != cache.dtype:
-        _refuse("q must be [batch, Hq, D] in the pool's type")
+    shape = _query_shape(cache, q, B)
     idx, top = _page_list(page_idx, cache, B)
     rc = lib().hymba_paged_select(cache.ref, ctypes.byref(tb), _int32_vector(seq_lens, B, "seq_lens"), q.data_ptr(),
-                                  qs, q.shape[1], n_first, n_last, top, idx, ws.data_ptr(), ws.numel(), st)
+                                  _head_rows(q, shape, "q"), shape[1], n_first, n_last, top, idx, ws.data_ptr(),
+                                  ws.numel(), st)
     if rc:
         check(rc)
 
@@ -399,19 +406,17 @@ def paged_attention(cache: PagedCache, q, table, seq_lens, out, ws, scale=None, 
     """hymba_paged_attention: out [B, Hq, D] = attention of one (rotated) query per sequence over
     the first seq_lens[b] positions of its pages; with window > 0 over the first n_meta positions
     and the last `window`; with page_idx over the listed pages.  scale: 1/sqrt(D) by default."""
-    st = _paged_stream(cache, stream, q, table, seq_lens, out, ws, page_idx, lse)
+    st = _paged_stream(cache, stream, (q, table, seq_lens, out, ws, page_idx, lse))
     tb, B = _page_table(table)
-    D = cache.head_dim
-    qs, os = _head_rows(q, D, "q"), _head_rows(out, D, "out")
-    Hq = q.shape[1]
-    if q.shape[0] != B or q.dtype != cache.dtype or out.shape != q.shape:
-        _refuse("q must be [batch, Hq, D] in the pool's type, and out shaped like it")
+    shape = _query_shape(cache, q, B)
+    Hq = shape[1]
     idx, top = (None, 0) if page_idx is None else _page_list(page_idx, cache, B)
-    if lse is not None and (lse.dtype != torch.float32 or lse.shape != (B, Hq) or not lse.is_contiguous()):
+    if lse is not None and (lse.dtype is not torch.float32 or lse.shape != (B, Hq) or not lse.is_contiguous()):
         _refuse("lse must be contiguous fp32 [batch, Hq]")
     rc = lib().hymba_paged_attention(cache.ref, ctypes.byref(tb), _int32_vector(seq_lens, B, "seq_lens"),
-                                     q.data_ptr(), qs, Hq, D ** -0.5 if scale is None else scale, n_meta, window, idx,
-                                     top, out.data_ptr(), _DT_CODE.get(out.dtype, -1), os,
+                                     q.data_ptr(), _head_rows(q, shape, "q"), Hq,
+                                     shape[2] ** -0.5 if scale is None else scale, n_meta, window, idx, top,
+                                     out.data_ptr(), _DT_CODE.get(out.dtype, -1), _head_rows(out, shape, "out"),
                                      None if lse is None else lse.data_ptr(), ws.data_ptr(), ws.numel(), st)
     if rc:
         check(rc)
@@ -575,7 +580,7 @@ def mixer_decode_paged(dims, dw: DeviceWeights, x, positions, cache: PagedCache,
                        top_pages=0, residual=None, stream=None, cfg=None):
     """hymba_mixer_decode over a paged cache: positions [B] int32, table [B, width] int32;
     top_pages > 0 (global layers): attention over that many selected pages."""
-    st = _paged_stream(cache, stream, x, positions, table, ssm_state, conv_state, out, ws, residual)
+    st = _paged_stream(cache, stream, (x, positions, table, ssm_state, conv_state, out, ws, residual))
     cfg = make_cfg(dims) if cfg is None else cfg
     tb, B = _page_table(table)
     if x.shape != (B, dims.d_model) or out.shape != x.shape or not (x.is_contiguous() and out.is_contiguous()):
