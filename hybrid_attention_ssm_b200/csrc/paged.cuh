@@ -1148,14 +1148,15 @@ __device__ __forceinline__ bool pa_arrive(const PagedAttnParams& p, int c0, int 
 }
 // After a wait that gave up, the counts are completed all the same, so that the next call on
 // the workspace finds them at zero: count this CTA's parts of cut items that it has not counted
-// (done: bit 0 an item begun earlier, bit 1 one that goes on), walking the items.
-__device__ __noinline__ void pa_arrive_rest(const PagedAttnParams& p, int t0, int t1, const PaShares& sh, int done) {
+// (done0: of an item begun earlier, done1: of one that goes on), walking the items.
+__device__ __noinline__ void pa_arrive_rest(const PagedAttnParams& p, int t0, int t1, const PaShares& sh, int done0,
+                                            int done1) {
   int beg = 0;
   for (int b = 0; b < p.B && beg < t1; ++b) {
     const int nt = pa_tiles(p, pa_len(p, b)).n_tiles;
     for (int g = 0; g < p.Hkv && beg < t1; ++g, beg += nt) {
       const int end = beg + nt;
-      if (end <= t0 || (beg >= t0 && end <= t1) || (done & (beg < t0 ? 1 : 2))) continue;
+      if (end <= t0 || (beg >= t0 && end <= t1) || (beg < t0 ? done0 : done1)) continue;
       const int c0 = sh.owner(beg);
       pa_arrive(p, c0, sh.owner(end - 1) - c0 + 1);
     }
@@ -1236,7 +1237,7 @@ __global__ void __launch_bounds__(PaShape<D, NHB>::THREADS, 1)
   };
   __shared__ PaPart pinfo[GROUPS][2];
   __shared__ int wsum[NWARPS];                       // tiles of a warp's sequences
-  __shared__ int counted, abort_flag;                // parts counted so far (bits as pa_arrive_rest)
+  __shared__ int counted[2], abort_flag;             // whether the part of slot 0 / 1 has been counted
   __shared__ PaPart joins[2];                        // the cut items that this CTA joins
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
@@ -1250,7 +1251,7 @@ __global__ void __launch_bounds__(PaShape<D, NHB>::THREADS, 1)
     }
     mbar_init(&fin_bar, CWARPS);
     joins[0].item = joins[1].item = -1;
-    abort_flag = counted = 0;
+    abort_flag = counted[0] = counted[1] = 0;
     fence_mbar_init();
     tma_prefetch_desc(&mapK);
     tma_prefetch_desc(&mapV);
@@ -1593,9 +1594,10 @@ __global__ void __launch_bounds__(PaShape<D, NHB>::THREADS, 1)
     // the item's tiles in this group are done: merge the four warps (2 and 3 into 0 and 1,
     // then 1 into 0), warp 0 writes the result or the part
     const int b = mt.item / p.Hkv, g = mt.item % p.Hkv;
-    // the end of an item that began in an earlier CTA, all of it here in the first group: its
-    // part is final now and leaves at once, while the rest streams on
-    const bool early = grp == 0 && mt.cut == 1 && mt.c0 != (int)blockIdx.x && mt.ends;
+    // a part of an item shared with other CTAs of which this group has all that is here (the
+    // end in the first group, the beginning in the last) leaves at once, while the rest goes on
+    const bool early =
+        mt.parts > 1 && (mt.cut == 1 ? grp == 0 && mt.c0 != (int)blockIdx.x && mt.ends : mt.cut == 2 && u1 == t1);
     float (*mo)[8][LD] = mos[grp];
 #pragma unroll
     for (int hb = 0; hb < NHB; ++hb) {
@@ -1646,7 +1648,8 @@ __global__ void __launch_bounds__(PaShape<D, NHB>::THREADS, 1)
           for (int j = 0; j < D / 8; ++j) store_pair(p.out, p.out_dt, at + 8 * j, acc[j][0] * inv, acc[j][1] * inv);
           if (p.lse != nullptr && tq == 0) p.lse[(long long)b * p.Hq + g * p.G + hh] = pa_lse(m, l);
         } else {
-          put(early ? p.part + ((long long)blockIdx.x * 2 * p.G + hh) * LD : part_row(grp, mt.cut - 1, hh));
+          put(early ? p.part + (((long long)blockIdx.x * 2 + mt.cut - 1) * p.G + hh) * LD
+                    : part_row(grp, mt.cut - 1, hh));
         }
       }
     }
@@ -1658,8 +1661,8 @@ __global__ void __launch_bounds__(PaShape<D, NHB>::THREADS, 1)
         pi.c0 = mt.c0;
         pi.parts = mt.parts;
         if (early) {
-          if (pa_arrive(p, mt.c0, mt.parts)) joins[0] = pi;   // joined when the CTA's groups are done
-          counted = 1;
+          if (pa_arrive(p, mt.c0, mt.parts)) joins[mt.cut - 1] = pi;   // joined when the CTA's groups are done
+          counted[mt.cut - 1] = 1;
         } else {
           pinfo[grp][mt.cut - 1] = pi;
         }
@@ -1706,9 +1709,9 @@ __global__ void __launch_bounds__(PaShape<D, NHB>::THREADS, 1)
         for (int f = 0; f < 2 * GROUPS; ++f) {
           const PaPart pi = pinfo[f >> 1][f & 1];
           const int slot = pi.c0 == (int)blockIdx.x ? 1 : 0;
-          if (pi.item >= 0 && pi.parts > 1 && !(counted & (1 << slot))) {   // (several groups' parts of one item)
+          if (pi.item >= 0 && pi.parts > 1 && !counted[slot]) {   // (several groups' parts of one item)
             if (pa_arrive(p, pi.c0, pi.parts)) joins[slot] = pi;
-            counted |= 1 << slot;
+            counted[slot] = 1;
           }
         }
       }
@@ -1721,7 +1724,7 @@ __global__ void __launch_bounds__(PaShape<D, NHB>::THREADS, 1)
       if (j.item >= 0) ok = pa_join<D, CWARPS>(p, j.item, j.c0, j.parts, tid, &mos[0][0][0][0], fin_sync);
     }
   }
-  if (!ok && tid == 0) pa_arrive_rest(p, t0, t1, shares, counted);
+  if (!ok && tid == 0) pa_arrive_rest(p, t0, t1, shares, counted[0], counted[1]);
 }
 
 }  // namespace hymba
