@@ -1019,7 +1019,7 @@ constexpr int PA_MAX_GRID = 148;   // CTAs (sizes the workspace)
 template <int D, int NHB>
 struct PaShape {
   static constexpr int GROUPS = NHB == 1 ? (D == 64 ? 3 : 2) : (D == 64 ? 2 : 1);
-  static constexpr int STAGES = NHB == 1 ? 3 : (D == 64 ? 4 : 5);
+  static constexpr int STAGES = D == 64 ? (NHB == 1 ? 3 : 4) : (NHB == 1 ? 2 : 5);
   static constexpr int CWARPS = 4 * GROUPS;                // consumer warps
   static constexpr int THREADS = (CWARPS + GROUPS) * 32;
   static constexpr int HALF = PA_KT * 128;                 // bytes of 64 positions x 64 dims

@@ -490,8 +490,8 @@ int hymba_paged_attention(const hymba_paged_kv* kv, const hymba_page_table* tabl
     return fail(HYMBA_ERR_INVALID_ARG, "seq_lens / q");
   if (out_dtype != HYMBA_DT_F32 && out_dtype != HYMBA_DT_BF16 && out_dtype != HYMBA_DT_F16)
     return fail(HYMBA_ERR_UNSUPPORTED, "output type %d", out_dtype);
-  if (out == nullptr || !aligned16(out) || out_stride < width || out_stride % 8 || !aligned4(lse))
-    return fail(HYMBA_ERR_INVALID_ARG, "out / lse");
+  if (out == nullptr || out == q || !aligned16(out) || out_stride < width || out_stride % 8 || !aligned4(lse))
+    return fail(HYMBA_ERR_INVALID_ARG, "out (NULL, q itself, misaligned, or its stride) / lse");
   if (!std::isfinite(scale)) return fail(HYMBA_ERR_INVALID_ARG, "scale %g", scale);
   if (n_meta < 0 || window < 0 || (window == 0 && n_meta > 0))
     return fail(HYMBA_ERR_INVALID_ARG, "n_meta %d, window %d (meta tokens go with a window)", n_meta, window);

@@ -364,6 +364,8 @@ def paged_append(cache: PagedCache, table, start, k, v, ws, q=None, q_out=None, 
     D = cache.head_dim
     src = k if k is not None else q
     dt, T = src.dtype, src.shape[0]
+    if T == 0 and cu_new is not None:
+        return
     kp = vp = qp = qo = None
     ks = vs = qs = Hq = 0
     if k is not None:

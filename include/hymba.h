@@ -354,7 +354,7 @@ int hymba_paged_workspace_size(const hymba_paged_kv* kv, int batch, int n_q_head
  *             q_stride elements apart (column slices of a fused projection): 16-byte aligned,
  *             strides multiples of 16 bytes.  k and v may be NULL together (only queries are
  *             rotated: a layer that reads another layer's cache), q and q_out likewise
- *   q_out     [n_tokens, Hq, D] in the pool's type
+ *   q_out     [n_tokens, Hq, D] in the pool's type; may be q itself (same type, rows contiguous)
  *   rope_base 0: no rotation (keys that were rotated before, e.g. a prefill cache's)
  * Page bounds, when the cache has them: a page whose row 0 is written in this call starts
  * over; otherwise the new keys widen its bounds.
@@ -398,7 +398,8 @@ int hymba_paged_select(const hymba_paged_kv* kv, const hymba_page_table* table, 
  * A sequence with no visible position gets zeros.  Values and keys at positions that are not
  * visible, NaN included, have no influence.
  *   q    rows of n_q_heads * D in the pool's type (n_q_heads up to 16 per KV head), q_stride
- *        apart (a multiple of 8); out likewise in out_dtype (F32, BF16 or F16), rounded once
+ *        apart (a multiple of 8); out likewise in out_dtype (F32, BF16 or F16), rounded once,
+ *        not overlapping q
  *   lse  [batch, n_q_heads] fp32, or NULL: log(sum_j exp(scale * q.k_j)), -inf for no position
  * Scores, probabilities and sums are fp32; the products with V take the probabilities as two
  * 16-bit halves.  The result does not depend on scheduling.  Work is shared out on the

@@ -365,6 +365,27 @@ def test_append_one_token_each_and_far_positions():
         assert torch.equal(cache.t["v"][b, :, s % ps].cpu(), v[b].to(dt))
 
 
+def test_append_in_place_and_of_nothing():
+    """Queries rotated where they are, in both kernels; a call without tokens changes nothing."""
+    ps, Hq, Hkv, D, dt = 16, 8, 2, 64, torch.float16
+    cache = H.PagedCache.zeros(20, ps, Hkv, D, dt, bounds=True)
+    table = torch.arange(20, dtype=torch.int32, device="cuda").view(2, 10)
+    i32 = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")
+    ws = H.alloc_workspace(256)
+    for new in ((1, 1), (70, 33)):
+        T = sum(new)
+        q, k = torch.randn(T, Hq, D, device="cuda").to(dt), torch.randn(T, Hkv, D, device="cuda").to(dt)
+        want = torch.empty_like(q)
+        cu = None if T == 2 else i32(0, new[0], T)
+        H.paged_append(cache, table, i32(3, 40), k, k, ws, q=q, q_out=want, cu_new=cu)
+        H.paged_append(cache, table, i32(3, 40), k, k, ws, q=q, q_out=q, cu_new=cu)
+        assert torch.equal(q, want)
+    before = cache.t["k"].clone()
+    H.paged_append(cache, table, i32(0, 0), k[:0], k[:0], ws, q=q[:0], q_out=q[:0], cu_new=i32(0, 0, 0))
+    H.paged_append(cache, table, i32(0, 0), k, k, ws, q=q, q_out=want, cu_new=i32(0, 0, 0))
+    assert torch.equal(before, cache.t["k"]) and H.status_read(ws) == H.OK
+
+
 def test_append_skips_what_has_no_place():
     """A position beyond the table, a bad page, a negative start: recorded, nothing stored for
     them, the others as ever.  Out-of-range fp16 values are recorded."""
@@ -602,7 +623,7 @@ def test_binding_refuses_what_it_can_see():
                 dict(seq_lens=ln.expand(2)), dict(out=out[:, :2]), dict(ws=ws[:512]), dict(lse=out[..., 0].half()),
                 dict(page_idx=torch.zeros(1, 2, 3, device="cuda")), dict(n_meta=4), dict(window=-1),
                 dict(scale=math.nan), dict(q=q.transpose(1, 2).contiguous().transpose(1, 2)),
-                dict(out=out.double()), dict(q=q[:, :3], out=out[:, :3])):
+                dict(out=out.double()), dict(q=q[:, :3], out=out[:, :3]), dict(out=q)):
         with pytest.raises(H.HymbaError):
             H.paged_attention(**{**good, **bad})
     with pytest.raises(H.HymbaError):                     # no page bounds
