@@ -128,9 +128,13 @@ int launch_paged_append(const hymba_paged_kv* kv, PagedAppendParams& p, float ro
   }
   p.rotate = rope_base > 0.f ? 1 : 0;
   const int h2 = kv->head_dim / 2;
-  for (int j = 0; p.rotate && j < h2; ++j) {   // the turn's fraction in units of 2^-64
-    const double t = std::exp2(-std::log2((double)rope_base) * j / h2) * 0.15915494309189535;
-    p.turns[j] = (unsigned long long)((t - std::floor(t)) * 18446744073709551616.0);
+  if (p.rotate) {   // turn_j = base^(-j / h2) / (2 pi), its fraction in units of 2^-64 (80-bit floats)
+    const long double step = std::exp2(-std::log2((long double)rope_base) / h2);
+    long double t = 0.159154943091895335768883763372514362L;
+    for (int j = 0; j < h2; ++j, t *= step) {
+      const long double f = t < 1.L ? t : t - std::floor(t);
+      p.turns[j] = (unsigned long long)(f * 18446744073709551616.0L);
+    }
   }
   // the most runs there can be (only a bound: the kernel counts them): a sequence of n tokens touches at most (n + 2 ps - 2) / ps
   // pages, and no more than it has tokens

@@ -296,7 +296,7 @@ def _paged_stream(cache, stream, tensors):
     that this is the device the library will launch on."""
     dev = cache.device
     for t in tensors:
-        if t is not None and t.get_device() != dev:
+        if t.get_device() != dev:
             _refuse(f"a tensor on {t.device}, the paged cache on cuda:{dev}")
     if stream is None:
         stream = torch.cuda.current_stream(dev)
@@ -359,7 +359,14 @@ def paged_append(cache: PagedCache, table, start, k, v, ws, q=None, q_out=None, 
     token per sequence).  k and v may be None together.  rope_base 0: no rotation."""
     if (k is None) != (v is None) or (q is None) != (q_out is None) or (k is None and q is None):
         _refuse("paged_append: k and v go together, q and q_out go together")
-    st = _paged_stream(cache, stream, (table, start, k, v, ws, q, q_out, cu_new))
+    tensors = [table, start, ws]
+    if k is not None:
+        tensors += (k, v)
+    if q is not None:
+        tensors += (q, q_out)
+    if cu_new is not None:
+        tensors.append(cu_new)
+    st = _paged_stream(cache, stream, tensors)
     tb, B = _page_table(table)
     D = cache.head_dim
     src = k if k is not None else q
@@ -369,10 +376,10 @@ def paged_append(cache: PagedCache, table, start, k, v, ws, q=None, q_out=None, 
     kp = vp = qp = qo = None
     ks = vs = qs = Hq = 0
     if k is not None:
-        shape = (T, cache.n_kv_heads, D)
-        kp, vp, ks, vs = k.data_ptr(), v.data_ptr(), _head_rows(k, shape, "k"), _head_rows(v, shape, "v")
         if v.dtype is not dt:
             _refuse(f"paged_append: k {dt}, v {v.dtype}")
+        shape = (T, cache.n_kv_heads, D)
+        kp, vp, ks, vs = k.data_ptr(), v.data_ptr(), _head_rows(k, shape, "k"), _head_rows(v, shape, "v")
     if q is not None:
         shape = q.shape
         if len(shape) != 3 or shape[0] != T or shape[2] != D or q.dtype is not dt:
@@ -408,7 +415,12 @@ def paged_attention(cache: PagedCache, q, table, seq_lens, out, ws, scale=None, 
     """hymba_paged_attention: out [B, Hq, D] = attention of one (rotated) query per sequence over
     the first seq_lens[b] positions of its pages; with window > 0 over the first n_meta positions
     and the last `window`; with page_idx over the listed pages.  scale: 1/sqrt(D) by default."""
-    st = _paged_stream(cache, stream, (q, table, seq_lens, out, ws, page_idx, lse))
+    tensors = [q, table, seq_lens, out, ws]
+    if page_idx is not None:
+        tensors.append(page_idx)
+    if lse is not None:
+        tensors.append(lse)
+    st = _paged_stream(cache, stream, tensors)
     tb, B = _page_table(table)
     shape = _query_shape(cache, q, B)
     Hq = shape[1]
@@ -582,7 +594,8 @@ def mixer_decode_paged(dims, dw: DeviceWeights, x, positions, cache: PagedCache,
                        top_pages=0, residual=None, stream=None, cfg=None):
     """hymba_mixer_decode over a paged cache: positions [B] int32, table [B, width] int32;
     top_pages > 0 (global layers): attention over that many selected pages."""
-    st = _paged_stream(cache, stream, (x, positions, table, ssm_state, conv_state, out, ws, residual))
+    st = _paged_stream(cache, stream, [t for t in (x, positions, table, ssm_state, conv_state, out, ws, residual)
+                                       if t is not None])
     cfg = make_cfg(dims) if cfg is None else cfg
     tb, B = _page_table(table)
     if x.shape != (B, dims.d_model) or out.shape != x.shape or not (x.is_contiguous() and out.is_contiguous()):

@@ -51,7 +51,7 @@ def select(kv=None, tb=None, **kw):
 
 
 def attention(kv=None, tb=None, **kw):
-    a = dict(lens=A, q=A, qs=256, hq=4, scale=0.125, meta=0, window=0, idx=None, top=0, out=A, odt=H.DT_F32, os=256,
+    a = dict(lens=A, q=A, qs=256, hq=4, scale=0.125, meta=0, window=0, idx=None, top=0, out=A + 4096, odt=H.DT_F32, os=256,
              lse=None, ws=A, wsb=1 << 30)
     a.update(kw)
     return H.lib().hymba_paged_attention(ctypes.byref(kv or cache()), ctypes.byref(tb or table()), a["lens"], a["q"],
@@ -112,7 +112,7 @@ def test_select_refusals(kw, code):
     (dict(hq=7), H.ERR_UNSUPPORTED), (dict(scale=math.nan), H.ERR_INVALID_ARG), (dict(scale=math.inf), H.ERR_INVALID_ARG),
     (dict(meta=-1), H.ERR_INVALID_ARG), (dict(meta=3), H.ERR_INVALID_ARG), (dict(window=-1), H.ERR_INVALID_ARG),
     (dict(idx=A, top=0), H.ERR_INVALID_ARG), (dict(idx=A, top=2, window=5), H.ERR_INVALID_ARG),
-    (dict(out=None), H.ERR_INVALID_ARG), (dict(out=A + 8), H.ERR_INVALID_ARG), (dict(odt=3), H.ERR_UNSUPPORTED),
+    (dict(out=None), H.ERR_INVALID_ARG), (dict(out=A), H.ERR_INVALID_ARG), (dict(out=A + 8), H.ERR_INVALID_ARG), (dict(odt=3), H.ERR_UNSUPPORTED),
     (dict(os=255), H.ERR_INVALID_ARG), (dict(lse=A + 1), H.ERR_INVALID_ARG), (dict(wsb=4096), H.ERR_WORKSPACE)])
 def test_attention_refusals(kw, code):
     assert attention(**kw) == code
