@@ -1717,11 +1717,12 @@ __global__ void __launch_bounds__(PaShape<D, NHB>::THREADS, 1)
       }
       if (ok) ok = fin_sync();
     }
-    // (the groups' parts have been merged and published: their merge rows are scratch now)
+    // (the rings are scratch now: every load has landed and been read; the groups' merge rows are
+    // not, another warp may still be reading the parts in them)
 #pragma unroll 1
     for (int s = 0; s < 2 && ok; ++s) {
       const PaPart j = joins[s];
-      if (j.item >= 0) ok = pa_join<D, CWARPS>(p, j.item, j.c0, j.parts, tid, &mos[0][0][0][0], fin_sync);
+      if (j.item >= 0) ok = pa_join<D, CWARPS>(p, j.item, j.c0, j.parts, tid, reinterpret_cast<float*>(rings), fin_sync);
     }
   }
   if (!ok && tid == 0) pa_arrive_rest(p, t0, t1, shares, counted[0], counted[1]);

@@ -190,6 +190,25 @@ def test_attention_split_and_joined(Hq, Hkv, D, ps, dt, lens):
     assert torch.equal(got, again) and torch.equal(lse, lse2)      # bit for bit
 
 
+@pytest.mark.parametrize("D,Hq,Hkv,dt", [(64, 25, 5, torch.float16), (128, 16, 4, torch.bfloat16),
+                                         (64, 12, 1, torch.float16)])
+def test_attention_items_cut_between_groups_and_ctas(D, Hq, Hkv, dt):
+    """About two items per CTA: nearly every CTA ends one, begins one and cuts others between its
+    groups, all at once.  Lengths shift from round to round, and every round must repeat itself."""
+    for r in range(6):
+        lens = [(977 * (i + 1) * (r + 1)) % 1800 for i in range(64)]
+        k, v, table = R.make_pool(lens, 64, Hkv, D, dt, seed=80 + r)
+        q = torch.randn(64, Hq, D, generator=torch.Generator().manual_seed(81 + r)).to(dt)
+        ref = R.attention(k, v, table, lens, q, D ** -0.5)
+        first = None
+        for _ in range(4):
+            got, lse, status = run_attention(k, v, table, lens, q)
+            assert status == H.OK
+            check_attention(got, lse, ref, v, max(lens), dt, torch.float32, D)
+            assert first is None or torch.equal(first, got)
+            first = got
+
+
 def test_attention_growing_maximum():
     """Scores that rise along the sequence, so every tile rescales what came before."""
     n, dt, D = 5000, torch.float16, 64
