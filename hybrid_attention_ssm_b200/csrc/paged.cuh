@@ -95,6 +95,12 @@ __device__ __forceinline__ void store_pair(void* out, int dt, long long i, float
 // contiguous shares instead: 61 -> 57 us at 4 x 8320 tokens).  A producer warp streams the items' rows through a ring by TMA, 8 tokens to a box, so
 // the bytes in flight cost neither registers nor instructions; eight consumer warps take a
 // stage's rows, 4 pairs of a row per thread.
+//
+// Bound by its bytes: 4 x 8320 tokens of 25 + 5 + 5 heads of 64 move 298 MB in 59 us, 5.0 TB/s
+// where a plain copy reaches 6.55 (45 us); ncu reads 57% of DRAM and half of the issue slots,
+// the rest is ramp and the mix of reads and writes.  Before the rows came by TMA (loads into
+// registers, a CTA per run) it took 140 us, then 64 with 4 pairs per thread in flight.  One
+// token for each of 64 sequences takes 6 us on the device, all of it latency.
 // ----------------------------------------------------------------------------------------
 constexpr int PAP_STEP_THREADS = 64;
 constexpr int PAP_CONSUMERS = 256;
@@ -690,6 +696,12 @@ __device__ __forceinline__ double q_scale() {   // 2^1000 or 2^880: |up| stays b
 // selection from the top digit down, on keys (the scores' bits in an order-preserving form)
 // rebased to the smallest one so that the first digit already spreads them, until at most 32
 // candidates share the digits of the last page taken; a warp ranks those.
+//
+// Bound by latency: a chain of length, table, bounds, cluster barrier and four block-wide
+// steps.  2049 pages x 5 heads of one sequence take 12 us, 64 sequences of up to 512 pages 14 us
+// (22 MB of bounds, 3.4 us at 6.55 TB/s); as two launches with a key buffer they took 20 and 24.
+// 512 threads per CTA were faster for one sequence (13.4 against 14.1 us cold) and slower for 64
+// (23.5 against 16.8), two page groups in flight instead of four slower for both.
 struct PagedSelectParams {
   const void *k_lo, *k_hi;   // [n_pages, Hkv, D]
   const void* q;             // [B] rows of Hq*D
@@ -1000,7 +1012,7 @@ __global__ void __launch_bounds__(PSEL_THREADS, 2)
 // item too it leaves one part in the workspace and counts it, and the CTA that completes the
 // count merges the parts in CTA order: the result does not depend on which one that is.  One
 // CTA per SM (instead of three small ones) keeps that last join to at most 148 parts and gives
-// it all of the CTA's threads.
+// it all of the CTA's threads (131073 keys of one sequence: 61 us with three, 44 with one).
 //
 // A group is a producer warp and four consumer warps with a ring of stages of their own.  The
 // producer walks the group's tiles: its lanes look up the pages and issue one TMA box per page
@@ -1012,6 +1024,14 @@ __global__ void __launch_bounds__(PSEL_THREADS, 2)
 // the rounding error of the probabilities (p = hi + lo, both 16 bits), so P V costs the same
 // number of instructions and keeps about twice the mantissa.  With 9 to 16 heads (NHB = 2)
 // rows 8..15 of Q K^T are heads 8..15, and P V runs once per 8 heads.
+//
+// Bound by the keys' and values' bytes, read once (ncu: 310 MB for 307).  Long runs stream at
+// 6.6 TB/s (2.7 GB in 410 us; a plain copy reaches 6.55), to which a call adds about 12 us:
+// 4 to the first copy, 2 to its data, the spread of the SMs at the end, and 3 to publish and
+// join cut items.  8 x 65537 keys in bf16 take 99 us (floor 88), 64 x up to 8320 59 (47), one
+// sequence of 131073 37 (26), a window of 1024 + 128 for 64 sequences 26 (15), 48 listed pages
+// of 32 for 64 31 (18).  A fourth stage or two groups of five changed nothing or cost 3%; two
+// stages are 3% slower at D = 64 and 1% faster at D = 128.
 // ----------------------------------------------------------------------------------------
 constexpr int PA_KT = 64;
 constexpr int PA_MAX_GRID = 148;   // CTAs (sizes the workspace)
