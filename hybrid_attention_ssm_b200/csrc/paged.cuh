@@ -92,9 +92,10 @@ __device__ __forceinline__ void store_pair(void* out, int dt, long long i, float
 // turn, a run being the tokens of one sequence that fall into one page: one CTA alone owns a
 // page's rows and bounds of a head, so there are no atomics and no second pass, and the heads
 // of a run, whose rows are neighbours in memory, are under way at the same time (equal
-// contiguous shares instead: 61 -> 57 us at 4 x 8320 tokens).  A producer warp streams the items' rows through a ring by TMA, 8 tokens to a box, so
-// the bytes in flight cost neither registers nor instructions; eight consumer warps take a
-// stage's rows, 4 pairs of a row per thread.
+// contiguous shares instead: 61 against 57 us at 4 x 8320 tokens).  A producer warp streams the
+// items' rows through a ring by TMA, 8 tokens to a box, so the bytes in flight cost neither
+// registers nor instructions; eight consumer warps take a stage's rows, 4 pairs of a row per
+// thread.
 //
 // Bound by its bytes: 4 x 8320 tokens of 25 + 5 + 5 heads of 64 move 298 MB in 59 us, 5.0 TB/s
 // where a plain copy reaches 6.55 (45 us); ncu reads 57% of DRAM and half of the issue slots,
@@ -119,7 +120,6 @@ struct PagedAppendParams {
   long long slice_stride;
   void* q_out;                      // [T, Hq, D] in the pool's type
   const int* start;                 // [B] position of each sequence's first new token
-  int start_add;                    // added to every start
   const int* cu_new;                // [B+1] first token row of each sequence, or NULL: one each
   const int* table;
   long long table_stride;
@@ -165,20 +165,26 @@ struct PapRaw<PDT_F32> {
     f[1] = f2_pack(r.z, r.w);
   }
 };
+// Rounded to the pool's type.  big: the largest magnitudes stored so far (fp16 pools).
 template <typename E>
-__device__ __forceinline__ uint2 pap_round(const uint64_t* f) {
-  return make_uint2(Elem<E>::pack(f2_lo(f[0]), f2_hi(f[0])), Elem<E>::pack(f2_lo(f[1]), f2_hi(f[1])));
+__device__ __forceinline__ void pap_keep(const uint2& a, uint32_t& big) {
+  if constexpr (Elem<E>::IS_F16) big = Elem<E>::max2(big, Elem<E>::max2(a.x & 0x7fff7fffu, a.y & 0x7fff7fffu));
+}
+template <typename E>
+__device__ __forceinline__ uint2 pap_round(const uint64_t* f, uint32_t& big) {
+  const uint2 a = make_uint2(Elem<E>::pack(f2_lo(f[0]), f2_hi(f[0])), Elem<E>::pack(f2_lo(f[1]), f2_hi(f[1])));
+  pap_keep<E>(a, big);
+  return a;
 }
 
-// cos and sin of pairs j0 .. j0 + N - 1 at a position, as packed fp32 pairs.  The phase's
+// cos and sin of the 4 pairs from j0 on at a position, as packed fp32 pairs.  The phase's
 // nearest quarter turn is split off in integers; the rest, at most 1/8 turn, goes into the
 // Taylor polynomials of sin(2 pi r) and cos(2 pi r) (remainders below 2e-9 and 2e-10).
-template <int N>
 struct PapTurn {
-  uint64_t cs[N / 2], sn[N / 2], neg[N / 2];   // neg = -sn
+  uint64_t cs[2], sn[2], neg[2];   // neg = -sn
   __device__ __forceinline__ void at(const PagedAppendParams& p, int pos, int j0) {
 #pragma unroll
-    for (int e = 0; e < N / 2; ++e) {
+    for (int e = 0; e < 2; ++e) {
       uint32_t quarter[2];
       float r[2];
 #pragma unroll
@@ -222,7 +228,7 @@ struct PapTurn {
 // head included; -1: no place), the group's query heads into q_out.  k returns the stored key
 // (low and high channels), big the largest magnitudes rounded so far.
 template <typename E, int D, int SRC>
-__device__ __forceinline__ void pap_token(const PagedAppendParams& p, const PapTurn<4>& turn, long long tok,
+__device__ __forceinline__ void pap_token(const PagedAppendParams& p, const PapTurn& turn, long long tok,
                                           long long row, int g, int part, uint2* k, uint32_t& big) {
   constexpr int H2 = D / 2, QB = 4;   // query heads whose loads are in flight together
   PapRaw<SRC> kr[2], vr[2], qr[QB][2];
@@ -244,10 +250,6 @@ __device__ __forceinline__ void pap_token(const PagedAppendParams& p, const PapT
     }
   };
   if (p.q != nullptr) load_q(0);
-  auto keep = [&](const uint2& a) {
-    if constexpr (Elem<E>::IS_F16)
-      big = Elem<E>::max2(big, Elem<E>::max2(a.x & 0x7fff7fffu, a.y & 0x7fff7fffu));
-  };
   auto rotate = [&](const PapRaw<SRC>* raw, uint2* out) {
     uint64_t a[2], b[2];
     raw[0].get(a);
@@ -256,26 +258,22 @@ __device__ __forceinline__ void pap_token(const PagedAppendParams& p, const PapT
 #pragma unroll
       for (int e = 0; e < 2; ++e) turn.apply(e, a[e], b[e]);
     }
-    out[0] = pap_round<E>(a);
-    out[1] = pap_round<E>(b);
-    keep(out[0]);
-    keep(out[1]);
+    out[0] = pap_round<E>(a, big);
+    out[1] = pap_round<E>(b, big);
   };
   if (row >= 0) {
     E* pv = static_cast<E*>(p.pv) + row + part * 4;
     if constexpr (std::is_same<typename PapRaw<SRC>::T, E>::value) {   // no rounding: the bits as they are
       *reinterpret_cast<uint2*>(pv) = vr[0].r;
       *reinterpret_cast<uint2*>(pv + H2) = vr[1].r;
-      keep(vr[0].r);
-      keep(vr[1].r);
+      pap_keep<E>(vr[0].r, big);
+      pap_keep<E>(vr[1].r, big);
     } else {
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         uint64_t f[2];
         vr[e].get(f);
-        const uint2 r = pap_round<E>(f);
-        *reinterpret_cast<uint2*>(pv + e * H2) = r;
-        keep(r);
+        *reinterpret_cast<uint2*>(pv + e * H2) = pap_round<E>(f, big);
       }
     }
     rotate(kr, k);
@@ -342,14 +340,14 @@ __global__ void __launch_bounds__(PAP_STEP_THREADS) paged_append_step_kernel(con
     for (long long k = i; k < p.n_clear; k += (long long)gridDim.x * PAP_STEP_THREADS) p.clear[k] = 0;
   if (bl >= p.B) return;
   const int b = (int)bl;
-  const int pos = p.start[b] + p.start_add;
+  const int pos = p.start[b];
   if (pos < 0) {   // refused whole: neither keys nor queries of this sequence
     report_error(p.status, DEV_ERR_BOUNDS, 612);
     return;
   }
   const int in_page = pos & ((1 << p.ps_log2) - 1);
   const int page = p.pk != nullptr ? pap_page(p, b, pos >> p.ps_log2) : -1;
-  PapTurn<4> turn;
+  PapTurn turn;
   if (p.rotate) turn.at(p, pos, part * 4);
   uint2 k[2];
   uint32_t big = 0;
@@ -367,10 +365,6 @@ __global__ void __launch_bounds__(PAP_STEP_THREADS) paged_append_step_kernel(con
 // New tokens of sequence b and its first token row; 0 tokens (and a report) where cu_new does
 // not name rows of this call.
 __device__ __forceinline__ int pap_count(const PagedAppendParams& p, int b, int* row0) {
-  if (p.cu_new == nullptr) {
-    *row0 = b;
-    return 1;
-  }
   const int r0 = p.cu_new[b], r1 = p.cu_new[b + 1];
   *row0 = r0;
   if (r0 < 0 || r1 < r0 || r1 > p.T) {
@@ -383,7 +377,7 @@ __device__ __forceinline__ int pap_count(const PagedAppendParams& p, int b, int*
 __device__ __forceinline__ int pap_runs(const PagedAppendParams& p, int b) {
   int r0;
   const int n = pap_count(p, b, &r0);
-  const int s = p.start[b] + p.start_add;
+  const int s = p.start[b];
   if (n == 0) return 0;
   if (s < 0 || s > 0x7fffffff - n) {   // refused whole: neither keys nor queries of this sequence
     report_error(p.status, DEV_ERR_BOUNDS, 612);
@@ -405,15 +399,6 @@ __device__ __forceinline__ void pap_get4(const uint8_t* s, uint64_t* f) {
     raw.get(f);
   }
 }
-// Rounded to the pool's type; big: the largest magnitudes rounded so far (fp16 pools)
-template <typename E>
-__device__ __forceinline__ uint2 pap_round(const uint64_t* f, uint32_t& big) {
-  const uint2 a = pap_round<E>(f);
-  if constexpr (Elem<E>::IS_F16)
-    big = Elem<E>::max2(big, Elem<E>::max2(a.x & 0x7fff7fffu, a.y & 0x7fff7fffu));
-  return a;
-}
-
 // what a stage's rows need besides their bytes
 struct PapMeta {
   long long row;     // element offset of the first row in the pool (head included), or -1: no place
@@ -484,7 +469,7 @@ __global__ void __launch_bounds__(PAP_THREADS, PAP_PER_SM)
     };
     while (ok && seek()) {
       int row0;
-      const int n = pap_count(p, b, &row0), s0 = p.start[b] + p.start_add;
+      const int n = pap_count(p, b, &row0), s0 = p.start[b];
       const int page_no = (s0 >> p.ps_log2) + run;          // page number within the sequence
       const int pos0 = run == 0 ? s0 : page_no << p.ps_log2;
       // (64-bit: the last page of the position range may end at 2^31)
@@ -583,7 +568,7 @@ __global__ void __launch_bounds__(PAP_THREADS, PAP_PER_SM)
     for (int i = tid; i < m.rows * PARTS; i += PAP_CONSUMERS) {
       const int r = i / PARTS, part = i % PARTS;
       const int at = r * HB + part * 4 * ESZ;
-      PapTurn<4> turn;
+      PapTurn turn;
       if (p.rotate) turn.at(p, m.pos + r, part * 4);
       auto rotate = [&](const uint8_t* s, uint2* out) {
         uint64_t a[2], c[2];

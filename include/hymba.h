@@ -362,7 +362,7 @@ int hymba_paged_workspace_size(const hymba_paged_kv* kv, int batch, int n_q_head
  * descending, a negative or too large start (that sequence is skipped), a position beyond the
  * table or a bad page (its keys and values are not stored); HYMBA_ERR_FP16_RANGE: a value that
  * an F16 pool cannot hold.
- * Two sequences that append to the same page race. */
+ * Table entries through which one call appends to the same page twice race. */
 int hymba_paged_append(const hymba_paged_kv* kv, const hymba_page_table* table, const int* start, const int* cu_new,
                        int n_tokens, int src_dtype, const void* k, long long k_stride, const void* v,
                        long long v_stride, const void* q, long long q_stride, int n_q_heads, void* q_out,
