@@ -1031,7 +1031,7 @@ struct PaShape {
   static constexpr int STAGE = 2 * (D / 64) * HALF;        // K then V
   static constexpr int QB = 8 * NHB * D * 2;
   static constexpr int LD = D + 4;                         // floats of a part's row: values, max, sum
-  static constexpr int SMEM = GROUPS * STAGES * STAGE + 1024;
+  static constexpr int SMEM = GROUPS * (STAGES * STAGE + 4 * 8 * LD * 4) + 1024;   // rings, merge rows, alignment
 };
 
 struct PagedAttnParams {
@@ -1108,6 +1108,8 @@ struct PaPart {
 };
 
 // (max, sum, 4 values) of a softmax over two sets of keys
+// of one query head; rows of D values, then the max and the sum
+template <int D>
 struct PaAcc {
   float m, l, x[4];
   __device__ void clear() {
@@ -1124,6 +1126,13 @@ struct PaAcc {
     x[2] = x[2] * wa + y.z * wb;
     x[3] = x[3] * wa + y.w * wb;
   }
+  __device__ void add(const float* row, int quad) {
+    add(row[D], row[D + 1], *reinterpret_cast<const float4*>(row + 4 * quad));
+  }
+  __device__ void put(float* row, int quad) const {
+    *reinterpret_cast<float4*>(row + 4 * quad) = make_float4(x[0], x[1], x[2], x[3]);
+    if (quad == 0) *reinterpret_cast<float2*>(row + D) = make_float2(m, l);
+  }
 };
 __device__ __forceinline__ float pa_inverse(float l) {   // no key: zeros; a NaN stays one
   return l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
@@ -1133,7 +1142,7 @@ __device__ __forceinline__ float pa_lse(float m, float l) {
 }
 // 4 values of query head hh of an item, and its lse
 template <int D>
-__device__ __forceinline__ void pa_finish(const PagedAttnParams& p, int item, int hh, int quad, const PaAcc& a) {
+__device__ __forceinline__ void pa_finish(const PagedAttnParams& p, int item, int hh, int quad, const PaAcc<D>& a) {
   const int b = item / p.Hkv, h = item % p.Hkv * p.G + hh;
   const float inv = pa_inverse(a.l);
   const long long at = b * p.out_stride + (long long)h * D + 4 * quad;
@@ -1180,7 +1189,7 @@ __device__ __forceinline__ bool pa_join(const PagedAttnParams& p, int item, int 
   const int heads = min(p.G, SUBS), per_head = SUBS / heads;   // heads at a time
   const int hs = sub / per_head, s0 = sub % per_head;
   for (int h0 = 0; h0 < p.G; h0 += heads) {
-    PaAcc a;
+    PaAcc<D> a;
     a.clear();
     if (hs < heads && h0 + hs < p.G) {
       const float* src = p.part + (((long long)c0 * 2) * p.G + h0 + hs) * LD;
@@ -1201,17 +1210,12 @@ __device__ __forceinline__ bool pa_join(const PagedAttnParams& p, int item, int 
           if (i0 + u * per_head < parts) a.add(ml[u].x, ml[u].y, x[u]);
       }
     }
-    float* row = sh + sub * LD;
-    *reinterpret_cast<float4*>(row + 4 * quad) = make_float4(a.x[0], a.x[1], a.x[2], a.x[3]);
-    if (quad == 0) *reinterpret_cast<float2*>(row + D) = make_float2(a.m, a.l);
+    a.put(sh + sub * LD, quad);
     if (!sync()) return false;
     if (sub < heads && h0 + sub < p.G) {
-      PaAcc t;
+      PaAcc<D> t;
       t.clear();
-      for (int k = 0; k < per_head; ++k) {
-        const float* r = sh + (sub * per_head + k) * LD;
-        t.add(r[D], r[D + 1], *reinterpret_cast<const float4*>(r + 4 * quad));
-      }
+      for (int k = 0; k < per_head; ++k) t.add(sh + (sub * per_head + k) * LD, quad);
       pa_finish<D>(p, item, h0 + sub, quad, t);
     }
     if (!sync()) return false;   // the rows are free again
@@ -1229,17 +1233,13 @@ __global__ void __launch_bounds__(PaShape<D, NHB>::THREADS, 1)
   constexpr int NWARPS = S::THREADS / 32;
   extern __shared__ uint8_t pa_smem_raw[];
   uint8_t* rings = align_smem<1024>(pa_smem_raw);
+  float (*mos)[4][8][LD] =                                             // a group's warps' parts of an item
+      reinterpret_cast<float (*)[4][8][LD]>(rings + GROUPS * STAGES * S::STAGE);
   __shared__ uint64_t full_bars[GROUPS][STAGES], empty_bars[GROUPS][STAGES], merge_bars[GROUPS], fin_bar;
   __shared__ __align__(16) PaMeta metas[GROUPS][STAGES];
   __shared__ __align__(128) uint8_t qbufs[GROUPS][2][S::QB];         // the queries of every other item
-  __shared__ __align__(16) float mos[GROUPS][2][8][LD];              // pairwise merge of a group's warps
-  // the groups' parts of cut items: one that ends in the group, one that goes on (the group's
-  // last item: with one block of heads it may stay in the merge rows)
-  __shared__ __align__(16) float prows[GROUPS][NHB][8 * NHB][LD];
-  auto part_row = [&](int k, int slot, int hh) -> float* {
-    if (NHB == 1 && slot == 1) return mos[k][0][hh];
-    return prows[k][slot][hh];
-  };
+  __shared__ __align__(16) float prows[GROUPS][2][8 * NHB][LD];      // the groups' parts of cut items: one
+                                                                     // begun earlier, one begun in the group
   __shared__ PaPart pinfo[GROUPS][2];
   __shared__ int wsum[NWARPS];                       // tiles of a warp's sequences
   __shared__ int counted[2], abort_flag;             // whether the part of slot 0 / 1 has been counted
@@ -1596,122 +1596,91 @@ __global__ void __launch_bounds__(PaShape<D, NHB>::THREADS, 1)
     }
     if (!ok) break;
 
-    // the item's tiles in this group are done: merge the four warps (2 and 3 into 0 and 1,
-    // then 1 into 0), warp 0 writes the result or the part
-    const int b = mt.item / p.Hkv, g = mt.item % p.Hkv;
+    // the item's tiles in this group are done: the four warps' states through shared memory,
+    // merged by 4 values per thread into the result or the group's part
+    constexpr int QUADS = D / 4;
     // a part of an item shared with other CTAs of which this group has all that is here (the
     // end in the first group, the beginning in the last) leaves at once, while the rest goes on
     const bool early =
         mt.parts > 1 && (mt.cut == 1 ? grp == 0 && mt.c0 != (int)blockIdx.x && mt.ends : mt.cut == 2 && u1 == t1);
-    float (*mo)[8][LD] = mos[grp];
 #pragma unroll
     for (int hb = 0; hb < NHB; ++hb) {
-      float m = m_run[hb], l = l_run[hb];
+      float l = l_run[hb];
       l += __shfl_xor_sync(0xffffffffu, l, 1);
       l += __shfl_xor_sync(0xffffffffu, l, 2);
-      float acc[D / 8][2];
+      float* row = mos[grp][wg][gq];
+      if (tq == 0) *reinterpret_cast<float2*>(row + D) = make_float2(m_run[hb], l);
 #pragma unroll
-      for (int j = 0; j < D / 8; ++j) {
-        acc[j][0] = o[hb][j][0] + o[hb][j][2];
-        acc[j][1] = o[hb][j][1] + o[hb][j][3];
-      }
-      auto put = [&](float* row) {
-        if (tq == 0) *reinterpret_cast<float2*>(row + D) = make_float2(m, l);
-#pragma unroll
-        for (int j = 0; j < D / 8; ++j)
-          *reinterpret_cast<float2*>(row + 8 * j + 2 * tq) = make_float2(acc[j][0], acc[j][1]);
-      };
-      auto take = [&](const float* row) {
-        const float m2 = row[D], l2 = row[D + 1];
-        const float mn = fmaxf(m, m2), mu = mn == -INFINITY ? 0.f : mn;
-        const float wa = ex2_approx(m - mu), wb = ex2_approx(m2 - mu);
-        m = mn;
-        l = l * wa + l2 * wb;
-#pragma unroll
-        for (int j = 0; j < D / 8; ++j) {
-          const float2 x = *reinterpret_cast<const float2*>(row + 8 * j + 2 * tq);
-          acc[j][0] = acc[j][0] * wa + x.x * wb;
-          acc[j][1] = acc[j][1] * wa + x.y * wb;
-        }
-      };
-      if (wg >= 2) put(mo[wg - 2][gq]);
+      for (int j = 0; j < D / 8; ++j)
+        *reinterpret_cast<float2*>(row + 8 * j + 2 * tq) =
+            make_float2(o[hb][j][0] + o[hb][j][2], o[hb][j][1] + o[hb][j][3]);
       ok = merge_sync();
       if (!ok) break;
-      if (wg < 2) take(mo[wg][gq]);
-      if (wg == 1) put(mo[1][gq]);   // slot 1 was warp 1's own to read
-      ok = merge_sync();
-      if (!ok) break;
-      if (wg == 0) take(mo[1][gq]);
-      ok = merge_sync();             // the slots are free again
-      if (!ok) break;
-      const int hh = hb * 8 + gq;    // query head within the group
-      if (wg == 0 && hh < p.G) {
-        if (mt.cut == 0) {
-          const float inv = pa_inverse(l);
-          const long long at = b * p.out_stride + (long long)(g * p.G + hh) * D + 2 * tq;
+      for (int k = tid & 127; k < min(8, p.G - hb * 8) * QUADS; k += 128) {
+        const int h = k / QUADS, quad = k % QUADS, hh = hb * 8 + h;   // query head within the group of heads
+        PaAcc<D> a;
+        a.clear();
 #pragma unroll
-          for (int j = 0; j < D / 8; ++j) store_pair(p.out, p.out_dt, at + 8 * j, acc[j][0] * inv, acc[j][1] * inv);
-          if (p.lse != nullptr && tq == 0) p.lse[(long long)b * p.Hq + g * p.G + hh] = pa_lse(m, l);
-        } else {
-          put(early ? p.part + (((long long)blockIdx.x * 2 + mt.cut - 1) * p.G + hh) * LD
-                    : part_row(grp, mt.cut - 1, hh));
-        }
+        for (int w = 0; w < 4; ++w) a.add(mos[grp][w][h], quad);
+        if (mt.cut == 0) pa_finish<D>(p, mt.item, hh, quad, a);
+        else if (early) a.put(p.part + (((long long)blockIdx.x * 2 + mt.cut - 1) * p.G + hh) * LD, quad);
+        else a.put(prows[grp][mt.cut - 1][hh], quad);
       }
+      ok = merge_sync();   // the rows are free again, the part is whole
+      if (!ok) break;
     }
-    if (ok && mt.cut != 0 && wg == 0) {
-      __syncwarp();
-      if (lane == 0) {
-        PaPart pi;
-        pi.item = mt.item;
-        pi.c0 = mt.c0;
-        pi.parts = mt.parts;
-        if (early) {
-          if (pa_arrive(p, mt.c0, mt.parts)) joins[mt.cut - 1] = pi;   // joined when the CTA's groups are done
-          counted[mt.cut - 1] = 1;
-        } else {
-          pinfo[grp][mt.cut - 1] = pi;
-        }
+    if (ok && mt.cut != 0 && wg == 0 && lane == 0) {
+      PaPart pi;
+      pi.item = mt.item;
+      pi.c0 = mt.c0;
+      pi.parts = mt.parts;
+      if (early) {
+        if (pa_arrive(p, mt.c0, mt.parts)) joins[mt.cut - 1] = pi;   // joined when the CTA's groups are done
+        counted[mt.cut - 1] = 1;
+      } else {
+        pinfo[grp][mt.cut - 1] = pi;
       }
     }
   }
 
   // ------------------------------ cut items ------------------------------
-  // The groups' parts in the order of the tiles; neighbours of one item are merged.  At most
-  // one item began in an earlier CTA (slot 0) and at most one goes on in a later one (slot 1).
+  // The groups' parts, in the order of the tiles; those of one item are neighbours and are merged.
+  // At most one item began in an earlier CTA (slot 0) and at most one goes on in a later one (1).
   if (ok) ok = fin_sync();
   if (ok) {
-    constexpr int QUADS = D / 4;
+    constexpr int QUADS = D / 4, NP = 2 * GROUPS;
+    int item[NP], heads[NP], n_items = 0;   // heads: a part that is the first of its item
     bool far = false;
-    for (int f = 0; f < 2 * GROUPS;) {
-      const PaPart pi = pinfo[f >> 1][f & 1];
-      int e = f + 1;
-      if (pi.item >= 0) {
-        while (e < 2 * GROUPS && (pinfo[e >> 1][e & 1].item == pi.item || pinfo[e >> 1][e & 1].item < 0)) ++e;
-        for (int k = tid; k < p.G * QUADS; k += CWARPS * 32) {
-          const int hh = k / QUADS, quad = k % QUADS;
-          PaAcc a;
-          a.clear();
-          for (int x = f; x < e; ++x) {
-            if (pinfo[x >> 1][x & 1].item < 0) continue;
-            const float* row = part_row(x >> 1, x & 1, hh);
-            a.add(row[D], row[D + 1], *reinterpret_cast<const float4*>(row + 4 * quad));
-          }
-          if (pi.parts == 1) {
-            pa_finish<D>(p, pi.item, hh, quad, a);
-          } else {
-            float* dst = p.part + (((long long)blockIdx.x * 2 + (pi.c0 == (int)blockIdx.x ? 1 : 0)) * p.G + hh) * LD;
-            *reinterpret_cast<float4*>(dst + 4 * quad) = make_float4(a.x[0], a.x[1], a.x[2], a.x[3]);
-            if (quad == 0) *reinterpret_cast<float2*>(dst + D) = make_float2(a.m, a.l);
-          }
-        }
-        far = far || pi.parts > 1;
+#pragma unroll
+    for (int f = 0, prev = -1; f < NP; ++f) {
+      item[f] = pinfo[f >> 1][f & 1].item;
+      heads[f] = item[f] >= 0 && item[f] != prev ? 1 : 0;
+      if (item[f] >= 0) {
+        prev = item[f];
+        far = far || pinfo[f >> 1][f & 1].parts > 1;
       }
-      f = e;
+      n_items += heads[f];
+    }
+    for (int k = tid; k < n_items * p.G * QUADS; k += CWARPS * 32) {
+      const int hq = k / QUADS, quad = k % QUADS, hh = hq % p.G;
+      int left = hq / p.G, first = 0;
+#pragma unroll
+      for (int f = 0; f < NP; ++f)
+        if (heads[f] && left-- == 0) first = f;
+      const PaPart pi = pinfo[first >> 1][first & 1];
+      PaAcc<D> a;
+      a.clear();
+#pragma unroll
+      for (int f = 0; f < NP; ++f)
+        if (item[f] == pi.item) a.add(prows[f >> 1][f & 1][hh], quad);
+      if (pi.parts == 1) pa_finish<D>(p, pi.item, hh, quad, a);
+      else a.put(p.part + (((long long)blockIdx.x * 2 + (pi.c0 == (int)blockIdx.x ? 1 : 0)) * p.G + hh) * LD, quad);
     }
     if (far) {
       ok = fin_sync();
       if (ok && tid == 0) {
-        for (int f = 0; f < 2 * GROUPS; ++f) {
+#pragma unroll 1
+        for (int f = 0; f < NP; ++f) {
           const PaPart pi = pinfo[f >> 1][f & 1];
           const int slot = pi.c0 == (int)blockIdx.x ? 1 : 0;
           if (pi.item >= 0 && pi.parts > 1 && !counted[slot]) {   // (several groups' parts of one item)
@@ -1722,12 +1691,13 @@ __global__ void __launch_bounds__(PaShape<D, NHB>::THREADS, 1)
       }
       if (ok) ok = fin_sync();
     }
-    // (the rings are scratch now: every load has landed and been read; the groups' merge rows are
-    // not, another warp may still be reading the parts in them)
+    // (the rings are scratch now: every load has landed and been read; the groups' part rows are
+    // not, another warp may still be reading them)
 #pragma unroll 1
     for (int s = 0; s < 2 && ok; ++s) {
       const PaPart j = joins[s];
-      if (j.item >= 0) ok = pa_join<D, CWARPS>(p, j.item, j.c0, j.parts, tid, reinterpret_cast<float*>(rings), fin_sync);
+      if (j.item >= 0)
+        ok = pa_join<D, CWARPS>(p, j.item, j.c0, j.parts, tid, reinterpret_cast<float*>(rings), fin_sync);
     }
   }
   if (!ok && tid == 0) pa_arrive_rest(p, t0, t1, shares, counted[0], counted[1]);
