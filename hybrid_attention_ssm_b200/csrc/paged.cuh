@@ -1177,46 +1177,58 @@ __device__ __noinline__ void pa_arrive_rest(const PagedAttnParams& p, int t0, in
   }
 }
 
-// Merge the CTAs' parts of an item, by the CTA's consumer threads: D / 4 lanes (4 values each)
-// per part and head, SUBS such groups of lanes, dealt evenly to the heads and among a head's
-// parts in a fixed order, then a head's groups through sh (a row of LD floats each).  The loads
-// go past L1, which may hold an older line of a neighbouring part.
+// Merge the CTAs' parts of n_jobs items, by the CTA's consumer threads: D / 4 lanes (4 values
+// each) per part and head, per_head such groups of lanes to a head, each with every per_head-th
+// part, then a head's groups through sh (a row of LD floats each).  per_head follows from an
+// item's parts alone (pa_join_width), so that the order of its sums does not depend on which
+// CTA joins it or what else that one has to join.  The loads go past L1, which may hold an older
+// line of a neighbouring part.
+constexpr int PA_JOIN_UN = 8;   // parts whose loads are in flight together
+template <int D, int CWARPS>
+__device__ __forceinline__ int pa_join_width(int parts, int G) {   // a batch of loads in one group, or all groups
+  constexpr int SUBS = CWARPS * 32 / (D / 4);
+  return parts <= PA_JOIN_UN ? 1 : SUBS / min(G, SUBS);
+}
 template <int D, int CWARPS, typename Sync>
-__device__ __forceinline__ bool pa_join(const PagedAttnParams& p, int item, int c0, int parts, int tid, float* sh,
-                                        Sync& sync) {
+__device__ __forceinline__ bool pa_join(const PagedAttnParams& p, const PaPart* jobs, int n_jobs, int per_head, int tid,
+                                        float* sh, Sync& sync) {
   constexpr int LPR = D / 4, SUBS = CWARPS * 32 / LPR, LD = D + 4;
   const int sub = tid / LPR, quad = tid % LPR;
-  const int heads = min(p.G, SUBS), per_head = SUBS / heads;   // heads at a time
+  const int n_heads = n_jobs * p.G, heads = min(n_heads, SUBS / per_head);   // heads: at a time
   const int hs = sub / per_head, s0 = sub % per_head;
-  for (int h0 = 0; h0 < p.G; h0 += heads) {
+#pragma unroll 1
+  for (int h0 = 0; h0 < n_heads; h0 += heads) {
     PaAcc<D> a;
     a.clear();
-    if (hs < heads && h0 + hs < p.G) {
-      const float* src = p.part + (((long long)c0 * 2) * p.G + h0 + hs) * LD;
-      constexpr int UN = 8;   // parts whose loads are in flight together
+    const int h = h0 + hs;
+    if (hs < heads && h < n_heads) {
+      const PaPart j = jobs[h / p.G];
+      const float* src = p.part + ((long long)j.c0 * 2 * p.G + h % p.G) * LD;
+      constexpr int UN = PA_JOIN_UN;
 #pragma unroll 1
-      for (int i0 = s0; i0 < parts; i0 += UN * per_head) {
+      for (int i0 = s0; i0 < j.parts; i0 += UN * per_head) {
         float2 ml[UN];
         float4 x[UN];
 #pragma unroll
         for (int u = 0; u < UN; ++u) {
-          const int i = min(i0 + u * per_head, parts - 1);   // (past the end: the last one, not added)
+          const int i = min(i0 + u * per_head, j.parts - 1);   // (past the end: the last one, not added)
           const float* row = src + ((long long)i * 2 + (i == 0 ? 1 : 0)) * p.G * LD;
           ml[u] = __ldcg(reinterpret_cast<const float2*>(row + D));
           x[u] = __ldcg(reinterpret_cast<const float4*>(row) + quad);
         }
 #pragma unroll
         for (int u = 0; u < UN; ++u)
-          if (i0 + u * per_head < parts) a.add(ml[u].x, ml[u].y, x[u]);
+          if (i0 + u * per_head < j.parts) a.add(ml[u].x, ml[u].y, x[u]);
       }
     }
     a.put(sh + sub * LD, quad);
     if (!sync()) return false;
-    if (sub < heads && h0 + sub < p.G) {
+    if (sub < heads && h0 + sub < n_heads) {
       PaAcc<D> t;
       t.clear();
+#pragma unroll 1
       for (int k = 0; k < per_head; ++k) t.add(sh + (sub * per_head + k) * LD, quad);
-      pa_finish<D>(p, item, h0 + sub, quad, t);
+      pa_finish<D>(p, jobs[(h0 + sub) / p.G].item, (h0 + sub) % p.G, quad, t);
     }
     if (!sync()) return false;   // the rows are free again
   }
@@ -1693,12 +1705,16 @@ __global__ void __launch_bounds__(PaShape<D, NHB>::THREADS, 1)
     }
     // (the rings are scratch now: every load has landed and been read; the groups' part rows are
     // not, another warp may still be reading them)
+    // two items of few parts are joined together
+    int width[2];
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+      width[s] = joins[s].item < 0 ? 0 : pa_join_width<D, CWARPS>(joins[s].parts, p.G);
+    const bool both = width[0] == 1 && width[1] == 1;
 #pragma unroll 1
-    for (int s = 0; s < 2 && ok; ++s) {
-      const PaPart j = joins[s];
-      if (j.item >= 0)
-        ok = pa_join<D, CWARPS>(p, j.item, j.c0, j.parts, tid, reinterpret_cast<float*>(rings), fin_sync);
-    }
+    for (int s = 0; s < 2 && ok; ++s)
+      if (width[s] > 0 && !(both && s == 1))
+        ok = pa_join<D, CWARPS>(p, joins + s, both ? 2 : 1, width[s], tid, reinterpret_cast<float*>(rings), fin_sync);
   }
   if (!ok && tid == 0) pa_arrive_rest(p, t0, t1, shares, counted[0], counted[1]);
 }
