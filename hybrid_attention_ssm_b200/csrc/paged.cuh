@@ -1011,12 +1011,12 @@ __global__ void __launch_bounds__(PSEL_THREADS, 2)
 // rows 8..15 of Q K^T are heads 8..15, and P V runs once per 8 heads.
 //
 // Bound by the keys' and values' bytes, read once (ncu: 310 MB for 307).  Long runs stream at
-// 6.6 TB/s (2.7 GB in 410 us; a plain copy reaches 6.55), to which a call adds about 12 us:
-// 4 to the first copy, 2 to its data, the spread of the SMs at the end, and 3 to publish and
-// join cut items.  8 x 65537 keys in bf16 take 99 us (floor 88), 64 x up to 8320 59 (47), one
-// sequence of 131073 37 (26), a window of 1024 + 128 for 64 sequences 26 (15), 48 listed pages
-// of 32 for 64 31 (18).  A fourth stage or two groups of five changed nothing or cost 3%; two
-// stages are 3% slower at D = 64 and 1% faster at D = 128.
+// 6.6 TB/s (2.7 GB in 410 us; a plain copy reaches 6.55), to which a call adds about 10 us: 3 to
+// the first copy, 2 to its data, the spread of the SMs at the end, and 3 to publish and join
+// cut items.  Back to back, 8 x 65537 keys in bf16 take 98 us (floor 88), 64 x up to 8320 57
+// (47), one sequence of 131073 37 (26), a window of 1024 + 128 for 64 sequences 24 (15), 48
+// listed pages of 32 for 64 30 (18).  A fourth stage or two groups of five changed nothing or
+// cost 3%; two stages are 3% slower at D = 64 and 1% faster at D = 128.
 // ----------------------------------------------------------------------------------------
 constexpr int PA_KT = 64;
 constexpr int PA_MAX_GRID = 148;   // CTAs (sizes the workspace)
@@ -1107,8 +1107,8 @@ struct PaPart {
   int c0, parts;
 };
 
-// (max, sum, 4 values) of a softmax over two sets of keys
-// of one query head; rows of D values, then the max and the sum
+// The running maximum and sum of a query head's softmax and 4 of its D weighted values; in memory
+// a row of D values, then the maximum and the sum.
 template <int D>
 struct PaAcc {
   float m, l, x[4];

@@ -291,6 +291,10 @@ def _refuse(msg):
     raise HymbaError(ERR_INVALID_ARG, msg)
 
 
+# the current stream's handle without the Stream object around it (1 us a call), where torch has it
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+
+
 def _paged_stream(cache, stream, tensors):
     """The stream to launch on, after checking that every tensor lives on the cache's device and
     that this is the device the library will launch on."""
@@ -298,26 +302,21 @@ def _paged_stream(cache, stream, tensors):
     for t in tensors:
         if t.get_device() != dev:
             _refuse(f"a tensor on {t.device}, the paged cache on cuda:{dev}")
-    if stream is None:
-        stream = torch.cuda.current_stream(dev)
-    if stream.device_index != dev or torch.cuda.current_device() != dev:
+    if torch.cuda.current_device() != dev or (stream is not None and stream.device_index != dev):
         _refuse(f"the paged cache is on cuda:{dev}, the current device or the stream is not")
-    return stream.cuda_stream
+    return _raw_stream(dev) if stream is None else stream.cuda_stream
 
 
-def _page_table(table):
-    st = table.stride()
+def _batch(table, vec, name):
+    """The batch's page table, its size, and the address of an int32 vector over it."""
+    st, shape = table.stride(), table.shape
     if len(st) != 2 or st[1] != 1 or table.dtype is not torch.int32:
         _refuse("block table must be int32 [batch, width] with contiguous rows")
-    B, width = table.shape
+    B, width = shape
+    if vec.dtype is not torch.int32 or vec.shape != (B,) or not vec.is_contiguous():
+        _refuse(f"{name} must be a contiguous int32 vector of {B}")
     # (a single row's stride is whatever torch made it)
-    return PageTable(table.data_ptr(), B, width, width if B == 1 else st[0]), B
-
-
-def _int32_vector(t, n, name):
-    if t.dtype is not torch.int32 or t.shape != (n,) or not t.is_contiguous():
-        _refuse(f"{name} must be a contiguous int32 vector of {n}")
-    return t.data_ptr()
+    return PageTable(table.data_ptr(), B, width, width if B == 1 else st[0]), B, vec.data_ptr()
 
 
 def _head_rows(t, shape, name):
@@ -325,14 +324,15 @@ def _head_rows(t, shape, name):
     st = t.stride()
     if t.shape != shape or st[2] != 1 or (st[1] != shape[2] and shape[1] != 1):
         _refuse(f"{name} must be {tuple(shape)} with contiguous heads, got {tuple(t.shape)}")
-    return shape[1] * shape[2] if shape[0] <= 1 else st[0]
+    return st[0] if shape[0] > 1 else shape[1] * shape[2]
 
 
-def _query_shape(cache, q, B):
+def _query_rows(cache, q, B):
+    """Shape and row stride of the queries of a decode call."""
     shape = q.shape
     if len(shape) != 3 or shape[0] != B or shape[2] != cache.head_dim or q.dtype is not cache.dtype:
         _refuse("q must be [batch, Hq, D] in the pool's type")
-    return shape
+    return shape, _head_rows(q, shape, "q")
 
 
 def _page_list(page_idx, cache, B):
@@ -367,12 +367,17 @@ def paged_append(cache: PagedCache, table, start, k, v, ws, q=None, q_out=None, 
     if cu_new is not None:
         tensors.append(cu_new)
     st = _paged_stream(cache, stream, tensors)
-    tb, B = _page_table(table)
+    tb, B, start_ptr = _batch(table, start, "start")
     D = cache.head_dim
     src = k if k is not None else q
     dt, T = src.dtype, src.shape[0]
-    if T == 0 and cu_new is not None:
-        return
+    cu_ptr = None
+    if cu_new is not None:
+        if cu_new.dtype is not torch.int32 or cu_new.shape != (B + 1,) or not cu_new.is_contiguous():
+            _refuse(f"cu_new must be a contiguous int32 vector of {B + 1}")
+        if T == 0:
+            return
+        cu_ptr = cu_new.data_ptr()
     kp = vp = qp = qo = None
     ks = vs = qs = Hq = 0
     if k is not None:
@@ -387,10 +392,8 @@ def paged_append(cache: PagedCache, table, start, k, v, ws, q=None, q_out=None, 
         if q_out.shape != shape or q_out.dtype is not cache.dtype or not q_out.is_contiguous():
             _refuse("paged_append: q_out must be contiguous, shaped like q, in the pool's type")
         qs, Hq, qp, qo = _head_rows(q, shape, "q"), shape[1], q.data_ptr(), q_out.data_ptr()
-    rc = lib().hymba_paged_append(cache.ref, ctypes.byref(tb), _int32_vector(start, B, "start"),
-                                  None if cu_new is None else _int32_vector(cu_new, B + 1, "cu_new"), T,
-                                  _DT_CODE.get(dt, -1), kp, ks, vp, vs, qp, qs, Hq, qo, rope_base, ws.data_ptr(),
-                                  ws.numel(), st)
+    rc = lib().hymba_paged_append(cache.ref, ctypes.byref(tb), start_ptr, cu_ptr, T, _DT_CODE.get(dt, -1), kp, ks, vp,
+                                  vs, qp, qs, Hq, qo, rope_base, ws.data_ptr(), ws.numel(), st)
     if rc:
         check(rc)
 
@@ -400,12 +403,11 @@ def paged_select(cache: PagedCache, q, table, seq_lens, page_idx, ws, n_first=1,
     pages (numbers within the sequence, ascending, -1 behind the last) that the rotated query
     q [B, Hq, D] should read: the first n_first, the last n_last and the best by page bounds."""
     st = _paged_stream(cache, stream, (q, table, seq_lens, page_idx, ws))
-    tb, B = _page_table(table)
-    shape = _query_shape(cache, q, B)
+    tb, B, lens = _batch(table, seq_lens, "seq_lens")
+    shape, qs = _query_rows(cache, q, B)
     idx, top = _page_list(page_idx, cache, B)
-    rc = lib().hymba_paged_select(cache.ref, ctypes.byref(tb), _int32_vector(seq_lens, B, "seq_lens"), q.data_ptr(),
-                                  _head_rows(q, shape, "q"), shape[1], n_first, n_last, top, idx, ws.data_ptr(),
-                                  ws.numel(), st)
+    rc = lib().hymba_paged_select(cache.ref, ctypes.byref(tb), lens, q.data_ptr(), qs, shape[1], n_first, n_last, top,
+                                  idx, ws.data_ptr(), ws.numel(), st)
     if rc:
         check(rc)
 
@@ -421,14 +423,13 @@ def paged_attention(cache: PagedCache, q, table, seq_lens, out, ws, scale=None, 
     if lse is not None:
         tensors.append(lse)
     st = _paged_stream(cache, stream, tensors)
-    tb, B = _page_table(table)
-    shape = _query_shape(cache, q, B)
+    tb, B, lens = _batch(table, seq_lens, "seq_lens")
+    shape, qs = _query_rows(cache, q, B)
     Hq = shape[1]
     idx, top = (None, 0) if page_idx is None else _page_list(page_idx, cache, B)
     if lse is not None and (lse.dtype is not torch.float32 or lse.shape != (B, Hq) or not lse.is_contiguous()):
         _refuse("lse must be contiguous fp32 [batch, Hq]")
-    rc = lib().hymba_paged_attention(cache.ref, ctypes.byref(tb), _int32_vector(seq_lens, B, "seq_lens"),
-                                     q.data_ptr(), _head_rows(q, shape, "q"), Hq,
+    rc = lib().hymba_paged_attention(cache.ref, ctypes.byref(tb), lens, q.data_ptr(), qs, Hq,
                                      shape[2] ** -0.5 if scale is None else scale, n_meta, window, idx, top,
                                      out.data_ptr(), _DT_CODE.get(out.dtype, -1), _head_rows(out, shape, "out"),
                                      None if lse is None else lse.data_ptr(), ws.data_ptr(), ws.numel(), st)
@@ -597,12 +598,11 @@ def mixer_decode_paged(dims, dw: DeviceWeights, x, positions, cache: PagedCache,
     st = _paged_stream(cache, stream, [t for t in (x, positions, table, ssm_state, conv_state, out, ws, residual)
                                        if t is not None])
     cfg = make_cfg(dims) if cfg is None else cfg
-    tb, B = _page_table(table)
+    tb, B, pos = _batch(table, positions, "positions")
     if x.shape != (B, dims.d_model) or out.shape != x.shape or not (x.is_contiguous() and out.is_contiguous()):
         _refuse("x and out must be contiguous [batch, d_model]")
-    check(lib().hymba_mixer_decode_paged(ctypes.byref(cfg), ctypes.byref(dw.c), ptr(x),
-                                         _int32_vector(positions, B, "positions"), cache.ref, ctypes.byref(tb),
-                                         top_pages, ptr(ssm_state), ptr(conv_state), ptr(residual), ptr(out), ptr(ws),
+    check(lib().hymba_mixer_decode_paged(ctypes.byref(cfg), ctypes.byref(dw.c), ptr(x), pos, cache.ref,
+                                         ctypes.byref(tb), top_pages, ptr(ssm_state), ptr(conv_state), ptr(residual), ptr(out), ptr(ws),
                                          ws.numel(), st))
 
 
