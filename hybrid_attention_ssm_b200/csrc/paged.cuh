@@ -1007,13 +1007,15 @@ __global__ void __launch_bounds__(PSEL_THREADS, 2)
 // of every tile each.  The item's query heads are rows of 16 x 16 x 8 tensor-core products:
 // rows 0..7 hold up to 8 heads, and rows 8..15, otherwise empty, take in the second product
 // the rounding error of the probabilities (p = hi + lo, both 16 bits), so P V costs the same
-// number of instructions and keeps about twice the mantissa.  With 9 to 16 heads (NHB = 2)
-// rows 8..15 of Q K^T are heads 8..15, and P V runs once per 8 heads.
+// number of instructions and keeps about twice the mantissa: 22 bits in fp16.  bf16's 16 show
+// in an fp32 output (1.2e-6 of it against 3.8e-7), so there, and only there, what is left goes
+// through a second product (97.8 -> 98.8 us at 8 x 65537 keys).  With 9 to 16 heads (NHB = 2) rows
+// 8..15 of Q K^T are heads 8..15, and P V runs once per 8 heads.
 //
 // Bound by the keys' and values' bytes, read once (ncu: 310 MB for 307).  Long runs stream at
 // 6.6 TB/s (2.7 GB in 410 us; a plain copy reaches 6.55), to which a call adds about 10 us: 3 to
 // the first copy, 2 to its data, the spread of the SMs at the end, and 3 to publish and join
-// cut items.  Back to back, 8 x 65537 keys in bf16 take 98 us (floor 88), 64 x up to 8320 57
+// cut items.  Back to back, 8 x 65537 keys in bf16 take 99 us (floor 88), 64 x up to 8320 57
 // (47), one sequence of 131073 37 (26), a window of 1024 + 128 for 64 sequences 24 (15), 48
 // listed pages of 32 for 64 30 (18).  A fourth stage or two groups of five changed nothing or
 // cost 3%; two stages are 3% slower at D = 64 and 1% faster at D = 128.
@@ -1484,6 +1486,7 @@ __global__ void __launch_bounds__(PaShape<D, NHB>::THREADS, 1)
   const int k_row = wg * 16 + (lane & 7) + ((lane >> 4) & 1) * 8, k_chk = (lane >> 3) & 1;
   const int v_row = wg * 16 + (lane & 7) + ((lane >> 3) & 1) * 8, v_chk = (lane >> 4) & 1;
   uint32_t merge_phase = 0, fin_phase = 0, phase = 0;
+  const bool third = !Elem<E>::IS_F16 && p.out_dt == PDT_F32;   // a third part of the probabilities
   int stg = 0, i = 0;
   bool ok = true;
   // barriers of the group's and of all consumer warps; bounded, so that a warp that gave up
@@ -1549,7 +1552,7 @@ __global__ void __launch_bounds__(PaShape<D, NHB>::THREADS, 1)
         // this lane's positions: 2tq, 2tq + 1, 2tq + 8, 2tq + 9 of the warp's 16
         const uint32_t mb = m16 >> (2 * tq);
         const bool vis[4] = {(mb & 1u) != 0, (mb & 2u) != 0, (mb & 0x100u) != 0, (mb & 0x200u) != 0};
-        uint32_t pa[NHB][4];
+        uint32_t pa[NHB][4], pb[NHB][2];   // p = hi + lo (+ the rest)
 #pragma unroll
         for (int hb = 0; hb < NHB; ++hb) {
           float v[4] = {s0[2 * hb] * p.scale_log2, s0[2 * hb + 1] * p.scale_log2, s1[2 * hb] * p.scale_log2,
@@ -1578,8 +1581,14 @@ __global__ void __launch_bounds__(PaShape<D, NHB>::THREADS, 1)
           pa[hb][0] = Elem<E>::pack(e[0], e[1]);
           pa[hb][2] = Elem<E>::pack(e[2], e[3]);
           const float2 h0 = Elem<E>::unpack(pa[hb][0]), h2 = Elem<E>::unpack(pa[hb][2]);
-          pa[hb][1] = Elem<E>::pack(e[0] - h0.x, e[1] - h0.y);
-          pa[hb][3] = Elem<E>::pack(e[2] - h2.x, e[3] - h2.y);
+          const float r[4] = {e[0] - h0.x, e[1] - h0.y, e[2] - h2.x, e[3] - h2.y};
+          pa[hb][1] = Elem<E>::pack(r[0], r[1]);
+          pa[hb][3] = Elem<E>::pack(r[2], r[3]);
+          if (third) {
+            const float2 l0 = Elem<E>::unpack(pa[hb][1]), l2 = Elem<E>::unpack(pa[hb][3]);
+            pb[hb][0] = Elem<E>::pack(r[0] - l0.x, r[1] - l0.y);
+            pb[hb][1] = Elem<E>::pack(r[2] - l2.x, r[3] - l2.y);
+          }
         }
         // a hidden position's probability is 0, but its value may be anything (0 * NaN): its
         // fragment halves are cleared
@@ -1596,6 +1605,10 @@ __global__ void __launch_bounds__(PaShape<D, NHB>::THREADS, 1)
           for (int hb = 0; hb < NHB; ++hb) {
             Elem<E>::mma(o[hb][j], pa[hb][0], pa[hb][1], pa[hb][2], pa[hb][3], f0, f1);
             Elem<E>::mma(o[hb][j + 1], pa[hb][0], pa[hb][1], pa[hb][2], pa[hb][3], f2, f3);
+            if (third) {
+              Elem<E>::mma(o[hb][j], pb[hb][0], 0u, pb[hb][1], 0u, f0, f1);
+              Elem<E>::mma(o[hb][j + 1], pb[hb][0], 0u, pb[hb][1], 0u, f2, f3);
+            }
           }
         }
       }

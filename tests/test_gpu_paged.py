@@ -8,7 +8,8 @@ Bounds, derived from the arithmetic (u16 = eps / 2 of the type, u = 2^-24):
   attention  scores: D products in fp32 accumulation, each step off by at most 2 u of the
              running size S = scale sum|q k|, then the scale and the subtraction of the maximum:
              d = (2 D + 8) u S in the exponent's argument, for numerator and denominator alike;
-             ex2.approx 4 u; the probability as two halves u16^2 (fp16: 2^-25 absolute on top);
+             ex2.approx 4 u; the probability as two 16-bit parts u16^2 (fp16: 2^-25 absolute on
+             top; bf16 has a third part);
              the sums over n keys in at most n + 64 steps of 2 u.  Relative to max|v|:
              c = 2 d + 2 (n + 64) u + 8 u + u16^2 + 2^-24, and the output's rounding u_out |ref|
 """
@@ -221,6 +222,33 @@ def test_attention_growing_maximum():
     got, lse, status = run_attention(k, v, table, [n], q)
     assert status == H.OK
     check_attention(got, lse, ref, v, n, dt, torch.float32, D)
+
+
+def test_attention_pool_halves_and_sliced_table():
+    """K and V as halves of one tensor's pages, a table that is a slice of a wider one, lengths
+    that are a slice of a longer vector, and a batch of nothing but empty sequences."""
+    ps, Hq, Hkv, D, dt, lens = 32, 10, 2, 64, torch.bfloat16, [100, 3, 260]
+    k, v, table = R.make_pool(lens, ps, Hkv, D, dt, seed=15)
+    both = torch.stack([k, v], 1).cuda()                       # [n_pages, 2, Hkv, page_size, D]
+    cache = H.PagedCache(both[:, 0], both[:, 1])
+    wide = torch.full((3, table.shape[1] + 5), -9, dtype=torch.int32)
+    wide[:, 2:2 + table.shape[1]] = table
+    tb = wide.cuda()[:, 2:2 + table.shape[1]]
+    ln = torch.tensor([7, 7] + lens + [7], dtype=torch.int32, device="cuda")[2:5]
+    q = torch.randn(3, Hq, D, generator=torch.Generator().manual_seed(16)).to(dt)
+    ws = workspace(cache, 3, Hq, table.shape[1])
+    out, lse = torch.empty(3, Hq, D, device="cuda"), torch.empty(3, Hq, device="cuda")
+    H.paged_attention(cache, q.cuda(), tb, ln, out, ws, lse=lse)
+    assert H.status_read(ws) == H.OK
+    check_attention(out.cpu(), lse.cpu(), R.attention(k, v, table, lens, q, D ** -0.5), v, 260, dt, torch.float32, D)
+    H.paged_attention(cache, q.cuda(), tb, torch.zeros_like(ln), out, ws, lse=lse)
+    assert H.status_read(ws) == H.OK and (out == 0).all() and (lse == -math.inf).all()
+    kv = torch.randn(3, Hkv, D, device="cuda").to(dt)          # append through the same views
+    H.paged_append(cache, tb, ln - 1, kv, kv, ws, rope_base=0.0)
+    assert H.status_read(ws) == H.OK
+    for b, n in enumerate(lens):
+        page, row = int(table[b, (n - 1) // ps]), (n - 1) % ps
+        assert torch.equal(both[page, 0, :, row], kv[b]) and torch.equal(both[page, 1, :, row], kv[b])
 
 
 def test_attention_strided_rows_and_bad_lengths():
