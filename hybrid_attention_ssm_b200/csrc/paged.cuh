@@ -1007,10 +1007,11 @@ __global__ void __launch_bounds__(PSEL_THREADS, 2)
 // of every tile each.  The item's query heads are rows of 16 x 16 x 8 tensor-core products:
 // rows 0..7 hold up to 8 heads, and rows 8..15, otherwise empty, take in the second product
 // the rounding error of the probabilities (p = hi + lo, both 16 bits), so P V costs the same
-// number of instructions and keeps about twice the mantissa: 22 bits in fp16.  bf16's 16 show
-// in an fp32 output (1.2e-6 of it against 3.8e-7), so there, and only there, what is left goes
-// through a second product (97.8 -> 98.8 us at 8 x 65537 keys).  With 9 to 16 heads (NHB = 2) rows
-// 8..15 of Q K^T are heads 8..15, and P V runs once per 8 heads.
+// number of instructions and keeps about twice the mantissa: 22 bits in fp16, of 2^15 p, so
+// that many small ones beside a large one count too (a bare p below 2^-25 would round to 0).
+// bf16's 16 bits show in an fp32 output (1.2e-6 of it against 3.8e-7), so there, and only there,
+// what is left goes through a second product (97.8 -> 98.8 us at 8 x 65537 keys).  With 9 to 16
+// heads (NHB = 2) rows 8..15 of Q K^T are heads 8..15, and P V runs once per 8 heads.
 //
 // Bound by the keys' and values' bytes, read once (ncu: 310 MB for 307).  Long runs stream at
 // 6.6 TB/s (2.7 GB in 410 us; a plain copy reaches 6.55), to which a call adds about 10 us: 3 to
@@ -1245,6 +1246,7 @@ __global__ void __launch_bounds__(PaShape<D, NHB>::THREADS, 1)
   constexpr int STAGES = S::STAGES, GROUPS = S::GROUPS, CWARPS = S::CWARPS, LD = S::LD;
   constexpr int NH = D / 64;
   constexpr int NWARPS = S::THREADS / 32;
+  constexpr float P_SCALE = Elem<E>::IS_F16 ? 32768.f : 1.f;   // of the probabilities in P V
   extern __shared__ uint8_t pa_smem_raw[];
   uint8_t* rings = align_smem<1024>(pa_smem_raw);
   float (*mos)[4][8][LD] =                                             // a group's warps' parts of an item
@@ -1578,6 +1580,10 @@ __global__ void __launch_bounds__(PaShape<D, NHB>::THREADS, 1)
               o[hb][j][0] *= al; o[hb][j][1] *= al; o[hb][j][2] *= al; o[hb][j][3] *= al;
             }
           }
+          if constexpr (Elem<E>::IS_F16) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) e[k] *= P_SCALE;
+          }
           pa[hb][0] = Elem<E>::pack(e[0], e[1]);
           pa[hb][2] = Elem<E>::pack(e[2], e[3]);
           const float2 h0 = Elem<E>::unpack(pa[hb][0]), h2 = Elem<E>::unpack(pa[hb][2]);
@@ -1638,7 +1644,7 @@ __global__ void __launch_bounds__(PaShape<D, NHB>::THREADS, 1)
 #pragma unroll
       for (int j = 0; j < D / 8; ++j)
         *reinterpret_cast<float2*>(row + 8 * j + 2 * tq) =
-            make_float2(o[hb][j][0] + o[hb][j][2], o[hb][j][1] + o[hb][j][3]);
+            make_float2((o[hb][j][0] + o[hb][j][2]) * (1.f / P_SCALE), (o[hb][j][1] + o[hb][j][3]) * (1.f / P_SCALE));
       ok = merge_sync();
       if (!ok) break;
       for (int k = tid & 127; k < min(8, p.G - hb * 8) * QUADS; k += 128) {

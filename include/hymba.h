@@ -402,9 +402,9 @@ int hymba_paged_select(const hymba_paged_kv* kv, const hymba_page_table* table, 
  *        not overlapping q
  *   lse  [batch, n_q_heads] fp32, or NULL: log(sum_j exp(scale * q.k_j)), -inf for no position
  * Scores, probabilities and sums are fp32; the products with V take the probabilities as two
- * 16-bit parts (three for an F32 output of a BF16 pool).  The result does not depend on scheduling.  Work is shared out on the
- * device from seq_lens, so a captured call serves any later lengths that the table can hold;
- * they must not change while the call runs.
+ * 16-bit parts (three for an F32 output of a BF16 pool).  The result does not depend on
+ * scheduling.  Work is shared out on the device from seq_lens, so a captured call serves any
+ * later lengths that the table can hold; they must not change while the call runs.
  * A length that is negative or beyond the table is recorded (HYMBA_ERR_INVALID_ARG) and
  * clamped; the positions of a page that is not in the pool are recorded and skipped. */
 int hymba_paged_attention(const hymba_paged_kv* kv, const hymba_page_table* table, const int* seq_lens, const void* q,

@@ -8,8 +8,9 @@ Bounds, derived from the arithmetic (u16 = eps / 2 of the type, u = 2^-24):
   attention  scores: D products in fp32 accumulation, each step off by at most 2 u of the
              running size S = scale sum|q k|, then the scale and the subtraction of the maximum:
              d = (2 D + 8) u S in the exponent's argument, for numerator and denominator alike;
-             ex2.approx 4 u; the probability as two 16-bit parts u16^2 (fp16: 2^-25 absolute on
-             top; bf16 has a third part);
+             ex2.approx 4 u; the probability as two 16-bit parts u16^2 (fp16: of 2^15 p, so 2^-40
+             absolute on top, below u for p > 2^-16 and added up at most n 2^-40; bf16 has a
+             third part);
              the sums over n keys in at most n + 64 steps of 2 u.  Relative to max|v|:
              c = 2 d + 2 (n + 64) u + 8 u + u16^2 + 2^-24, and the output's rounding u_out |ref|
 """
@@ -222,6 +223,31 @@ def test_attention_growing_maximum():
     got, lse, status = run_attention(k, v, table, [n], q)
     assert status == H.OK
     check_attention(got, lse, ref, v, n, dt, torch.float32, D)
+
+
+@pytest.mark.parametrize("D,Hq,Hkv,dt", [(64, 5, 1, torch.float16), (128, 9, 1, torch.float16), (64, 2, 2, torch.bfloat16)])
+def test_attention_small_probabilities_add_up(D, Hq, Hkv, dt):
+    """One key of every 16 takes nearly all of the weight and has the value 0; the others, each
+    e^-17.5 of it (below half of fp16's smallest step), make the whole result.  Values are not
+    negative, so the bound of check_attention holds relative to the result itself: it is
+    c sum_j p_j |v_j| before max|v| is put in its place."""
+    n, ps = 1500, 64
+    k, v, table = R.make_pool([n], ps, Hkv, D, dt, seed=31)
+    k[k.isfinite()] = 0
+    v[v.isfinite()] = v[v.isfinite()].abs().clamp(0.25, 2)
+    big = torch.arange(0, n, 16)
+    page = table[0].long()[big // ps]
+    k[page, :, big % ps, 0] = 1
+    v[page, :, big % ps] = 0
+    q = torch.zeros(1, Hq, D, dtype=dt)
+    q[..., 0] = 17.5
+    out, _, size = R.attention(k, v, table, [n], q, 1.0)
+    got, _, status = run_attention(k, v, table, [n], q, scale=1.0)
+    assert status == H.OK
+    small = 2.0 ** -40 * math.exp(17.5) if dt == torch.float16 else 0   # of the parts of p
+    c = 2 * (2 * D + 8) * U * size[..., None] + (2 * (n + 64) + 8) * U + half_step(dt) ** 2 + U + small
+    err = (got.double() - out).abs()
+    assert (err <= (c + U) * out).all(), f"worst {float((err / out).max()):.2e} of the result"
 
 
 def test_attention_pool_halves_and_sliced_table():
