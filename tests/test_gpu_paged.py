@@ -153,6 +153,22 @@ def test_visible_nan_and_infinite_keys():
     assert torch.isfinite(got[2]).all()
 
 
+@pytest.mark.parametrize("dt", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("bad", [math.inf, -math.inf, math.nan])
+def test_visible_value_that_is_not_finite(dt, bad):
+    """Its channel in the heads of its group is not finite either; all else is as without it."""
+    lens, ps, Hq, Hkv, D = [40, 90], 16, 6, 2, 64
+    k, v, table = R.make_pool(lens, ps, Hkv, D, dt, seed=33)
+    q = torch.randn(2, Hq, D, generator=torch.Generator().manual_seed(34)).to(dt)
+    want, wl, _ = run_attention(k, v, table, lens, q)
+    v[table[1, 2].long(), 1, 5, 7] = bad
+    got, lse, status = run_attention(k, v, table, lens, q)
+    assert status == H.OK and torch.equal(lse, wl)
+    assert not got[1, 3:, 7].isfinite().any()
+    got[1, 3:, 7] = want[1, 3:, 7]
+    assert torch.equal(got, want)
+
+
 @pytest.mark.parametrize("ps,top,dt,Hq,Hkv,D", [(16, 5, torch.float16, 10, 2, 64), (32, 3, torch.bfloat16, 25, 5, 64),
                                                 (64, 4, torch.float16, 8, 1, 128), (128, 2, torch.float16, 12, 1, 64)])
 def test_attention_listed_pages(ps, top, dt, Hq, Hkv, D):
