@@ -1075,7 +1075,7 @@ __device__ __forceinline__ PaTiles pa_tiles(const PagedAttnParams& p, int raw_le
     r.n_tiles = (int)((rows + PA_KT - 1) / PA_KT);
   } else if (p.W > 0) {
     const int w0 = max(0, r.len - p.W) / PA_KT;           // the window's first tile
-    r.head = min(w0, (p.M + PA_KT - 1) / PA_KT);
+    r.head = min(w0, (int)(((unsigned)p.M + PA_KT - 1) / PA_KT));   // (M may be up to 2^31 - 1)
     r.skip = w0 - r.head;
     r.n_tiles = all - r.skip;
   }
