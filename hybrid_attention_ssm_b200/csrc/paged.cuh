@@ -1163,17 +1163,19 @@ __device__ __forceinline__ bool pa_arrive(const PagedAttnParams& p, int c0, int 
                : "=r"(old) : "l"(p.arrived + c0), "r"((unsigned)(parts - 1)) : "memory");
   return old == (unsigned)(parts - 1);
 }
+// A CTA counts each of its two parts once: whoever takes its flag does.  (After a wait that gave
+// up, another group may still be on its way to publish.)
+__device__ __forceinline__ bool pa_claim(int* counted) { return atomicExch(counted, 1) == 0; }
 // After a wait that gave up, the counts are completed all the same, so that the next call on
-// the workspace finds them at zero: count this CTA's parts of cut items that it has not counted
-// (done0: of an item begun earlier, done1: of one that goes on), walking the items.
-__device__ __noinline__ void pa_arrive_rest(const PagedAttnParams& p, int t0, int t1, const PaShares& sh, int done0,
-                                            int done1) {
+// the workspace finds them at zero: count this CTA's parts of cut items that nobody has claimed
+// (counted[0]: of an item begun earlier, [1]: of one that goes on), walking the items.
+__device__ __noinline__ void pa_arrive_rest(const PagedAttnParams& p, int t0, int t1, const PaShares& sh, int* counted) {
   int beg = 0;
   for (int b = 0; b < p.B && beg < t1; ++b) {
     const int nt = pa_tiles(p, pa_len(p, b)).n_tiles;
     for (int g = 0; g < p.Hkv && beg < t1; ++g, beg += nt) {
       const int end = beg + nt;
-      if (end <= t0 || (beg >= t0 && end <= t1) || (beg < t0 ? done0 : done1)) continue;
+      if (end <= t0 || (beg >= t0 && end <= t1) || !pa_claim(counted + (beg < t0 ? 0 : 1))) continue;
       const int c0 = sh.owner(beg);
       pa_arrive(p, c0, sh.owner(end - 1) - c0 + 1);
     }
@@ -1258,7 +1260,7 @@ __global__ void __launch_bounds__(PaShape<D, NHB>::THREADS, 1)
                                                                      // begun earlier, one begun in the group
   __shared__ PaPart pinfo[GROUPS][2];
   __shared__ int wsum[NWARPS];                       // tiles of a warp's sequences
-  __shared__ int counted[2], abort_flag;             // whether the part of slot 0 / 1 has been counted
+  __shared__ int counted[2], abort_flag;             // whether the part of slot 0 / 1 is counted (pa_claim)
   __shared__ PaPart joins[2];                        // the cut items that this CTA joins
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
@@ -1666,8 +1668,8 @@ __global__ void __launch_bounds__(PaShape<D, NHB>::THREADS, 1)
       pi.c0 = mt.c0;
       pi.parts = mt.parts;
       if (early) {
-        if (pa_arrive(p, mt.c0, mt.parts)) joins[mt.cut - 1] = pi;   // joined when the CTA's groups are done
-        counted[mt.cut - 1] = 1;
+        if (pa_claim(counted + mt.cut - 1) && pa_arrive(p, mt.c0, mt.parts))
+          joins[mt.cut - 1] = pi;                    // joined when the CTA's groups are done
       } else {
         pinfo[grp][mt.cut - 1] = pi;
       }
@@ -1714,9 +1716,8 @@ __global__ void __launch_bounds__(PaShape<D, NHB>::THREADS, 1)
         for (int f = 0; f < NP; ++f) {
           const PaPart pi = pinfo[f >> 1][f & 1];
           const int slot = pi.c0 == (int)blockIdx.x ? 1 : 0;
-          if (pi.item >= 0 && pi.parts > 1 && !counted[slot]) {   // (several groups' parts of one item)
+          if (pi.item >= 0 && pi.parts > 1 && pa_claim(counted + slot)) {   // (several groups' parts of one item)
             if (pa_arrive(p, pi.c0, pi.parts)) joins[slot] = pi;
-            counted[slot] = 1;
           }
         }
       }
@@ -1735,7 +1736,7 @@ __global__ void __launch_bounds__(PaShape<D, NHB>::THREADS, 1)
       if (width[s] > 0 && !(both && s == 1))
         ok = pa_join<D, CWARPS>(p, joins + s, both ? 2 : 1, width[s], tid, reinterpret_cast<float*>(rings), fin_sync);
   }
-  if (!ok && tid == 0) pa_arrive_rest(p, t0, t1, shares, counted[0], counted[1]);
+  if (!ok && tid == 0) pa_arrive_rest(p, t0, t1, shares, counted);
 }
 
 }  // namespace hymba
