@@ -21,7 +21,7 @@ enum : unsigned {
 struct DevStatus {
   unsigned flags;      // OR of DEV_ERR_*
   unsigned site;       // id of the last wait/check that failed
-  unsigned pad[62];
+  unsigned parts[62];  // the paged attention's part counters, 8 bits each: zero between calls
 };
 
 // Wait limit in nanoseconds for every spin on an mbarrier (set from the host).

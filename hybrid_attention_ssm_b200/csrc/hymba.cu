@@ -68,11 +68,6 @@ cudaError_t launch_pdl(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t sme
   return cudaLaunchKernelEx(&cfg, kern, std::forward<Args>(args)...);
 }
 
-// What hymba_workspace_init zeroes: the status word, and the counters that follow it in the
-// workspaces of the paged calls.
-constexpr size_t WS_INIT_BYTES = 4096;
-static_assert(256 + PA_MAX_GRID * sizeof(unsigned) <= WS_INIT_BYTES, "the paged attention's counters");
-
 inline size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 // threads of splitk_sum_rmsnorm_kernel for rows of d: one 16-byte piece each, whole warps
 inline int snorm_threads(int d) { return ((d / 4 + 31) / 32) * 32; }
@@ -824,7 +819,7 @@ int hymba_decode_stage_layout(const hymba_layer_cfg* cfg, int batch, int max_tok
 int hymba_workspace_init(void* ws, size_t ws_bytes, hymba_stream stream) {
   if (ws == nullptr || ws_bytes < 256 || (reinterpret_cast<uintptr_t>(ws) & 255u))
     return fail(HYMBA_ERR_INVALID_ARG, "workspace NULL, < 256 bytes or not 256-byte aligned");
-  HY_CUDA(cudaMemsetAsync(ws, 0, std::min(ws_bytes, WS_INIT_BYTES), (cudaStream_t)stream));
+  HY_CUDA(cudaMemsetAsync(ws, 0, sizeof(DevStatus), (cudaStream_t)stream));
   return HYMBA_OK;
 }
 
@@ -833,7 +828,7 @@ int hymba_status_read(void* ws, hymba_stream stream, int* status) {
   DevStatus h;
   HY_CUDA(cudaStreamSynchronize((cudaStream_t)stream));
   HY_CUDA(cudaMemcpy(&h, ws, sizeof(unsigned) * 2, cudaMemcpyDeviceToHost));
-  HY_CUDA(cudaMemset(ws, 0, 256));
+  HY_CUDA(cudaMemset(ws, 0, sizeof(unsigned) * 2));   // (not the counters: another stream may be in a call)
   *status = (h.flags & DEV_ERR_TIMEOUT)      ? HYMBA_ERR_TIMEOUT
             : (h.flags & DEV_ERR_FP16_RANGE) ? HYMBA_ERR_FP16_RANGE
             : (h.flags & DEV_ERR_BOUNDS)     ? HYMBA_ERR_INVALID_ARG

@@ -129,7 +129,8 @@ struct PagedAppendParams {
   long long page_stride, head_stride, row_stride;
   void *k_lo, *k_hi;                // [n_pages, Hkv, D], or NULL
   unsigned* clear;                  // n_clear words that the step kernel zeroes (the counters of an
-  int n_clear;                      // attention that follows in the same call), or NULL
+  int n_clear;                      // attention that follows in the same call: it then needs no
+                                    // initialised workspace), or NULL
   DevStatus* status;
   unsigned long long turns[64];     // theta_j / (2 pi) in units of 2^-64
 };
@@ -1023,6 +1024,9 @@ __global__ void __launch_bounds__(PSEL_THREADS, 2)
 // ----------------------------------------------------------------------------------------
 constexpr int PA_KT = 64;
 constexpr int PA_MAX_GRID = 148;   // CTAs (sizes the workspace)
+constexpr int PA_PART_WORDS = (PA_MAX_GRID + 3) / 4;   // words of the CTAs' part counters in the status
+static_assert(PA_MAX_GRID < 256 && PA_PART_WORDS <= sizeof(DevStatus::parts) / sizeof(unsigned),
+              "a counter counts up to one part per CTA in 8 bits");
 
 template <int D, int NHB>
 struct PaShape {
@@ -1053,8 +1057,7 @@ struct PagedAttnParams {
   int dim_row, dim_head;      // tensor-map dimensions (1..3) of rows and heads; pages have the other
   float scale_log2;
   float* part;                // [grid][2][G][D + 4]: slot 1 the item that begins in the CTA
-  unsigned* arrived;          // [grid], zero between calls: parts of the cut item that CTA began
-  DevStatus* status;
+  DevStatus* status;          // its counter c: parts of the cut item that CTA c began
 };
 
 struct PaTiles {
@@ -1156,12 +1159,17 @@ __device__ __forceinline__ void pa_finish(const PagedAttnParams& p, int item, in
 
 // Count a part of the item that CTA c0 began; true for the last of `parts`, which also returns
 // the counter to zero.  Releases what the caller's CTA wrote before (after a barrier), and
-// acquires what the others did.
+// acquires what the others did.  Four counters share a word: they lie in the status, which every
+// workspace has and no other call touches, so a workspace may serve calls of other kinds in
+// between.
 __device__ __forceinline__ bool pa_arrive(const PagedAttnParams& p, int c0, int parts) {
+  unsigned* word = p.status->parts + c0 / 4;
+  const int sh = c0 % 4 * 8;
   unsigned old;
-  asm volatile("atom.acq_rel.gpu.global.inc.u32 %0, [%1], %2;"
-               : "=r"(old) : "l"(p.arrived + c0), "r"((unsigned)(parts - 1)) : "memory");
-  return old == (unsigned)(parts - 1);
+  asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], %2;" : "=r"(old) : "l"(word), "r"(1u << sh) : "memory");
+  if (((old >> sh) & 255u) != (unsigned)(parts - 1)) return false;
+  atomicSub(word, (unsigned)parts << sh);
+  return true;
 }
 // A CTA counts each of its two parts once: whoever takes its flag does.  (After a wait that gave
 // up, another group may still be on its way to publish.)

@@ -7,14 +7,12 @@ namespace {
 constexpr int PAGED_MAX_SELECT_WIDTH = 16384;   // one CTA ranks a sequence's pages in shared memory
 
 struct PagedWs {
-  size_t arrived, part, total;
+  size_t part, total;
 };
-// The attention's part counters follow the status word (hymba_workspace_init zeroes both, and
-// every call leaves the counters at zero), then its parts.  The other calls use the status word.
+// The attention's parts follow the status word.  The other calls use the status word only.
 PagedWs paged_layout(int head_dim, int group) {
   PagedWs w;
-  w.arrived = 256;
-  w.part = align256(w.arrived + (size_t)PA_MAX_GRID * sizeof(unsigned));
+  w.part = 256;
   w.total = align256(w.part + (size_t)PA_MAX_GRID * 2 * group * (head_dim + 4) * 4);
   return w;
 }
@@ -228,7 +226,6 @@ int launch_paged_attn(const hymba_paged_kv* kv, PagedAttnParams& p, uint8_t* ws,
   p.n_pages = kv->n_pages;
   p.ps_log2 = log2_int(kv->page_size);
   p.cap = paged_cap(p.width, kv->page_size);
-  p.arrived = reinterpret_cast<unsigned*>(ws + L.arrived);
   p.part = reinterpret_cast<float*>(ws + L.part);
   // tiles are counted in 32 bits (2^31 of them are 16 TB of keys of one head)
   const long long reach = p.page_idx != nullptr ? std::min(p.top, p.width) : p.width;
@@ -312,7 +309,7 @@ struct PagedDecode {
 };
 // Workspace after the decode step's own buffers (laid out as for one key: no key splits).
 struct PagedDecodeWs {
-  size_t q, arrived, part, idx, total;
+  size_t q, part, idx, total;
 };
 DecodeWs paged_decode_base(const Dims& m, int B) { return decode_layout(m, B, true, 1); }
 PagedDecodeWs paged_decode_layout(const Dims& m, int B, int top_pages) {
@@ -320,7 +317,6 @@ PagedDecodeWs paged_decode_layout(const Dims& m, int B, int top_pages) {
   size_t off = paged_decode_base(m, B).total;
   auto take = [&](size_t bytes) { size_t o = off; off = align256(off + bytes); return o; };
   w.q = take((size_t)B * m.qw * 2);
-  w.arrived = take((size_t)PA_MAX_GRID * sizeof(unsigned));
   w.part = take((size_t)PA_MAX_GRID * 2 * (m.Hq / m.Hkv) * (m.D + 4) * 4);
   w.idx = take((size_t)B * m.Hkv * top_pages * 4);
   w.total = off;
@@ -342,8 +338,7 @@ int check_paged_decode(const PagedDecode& d, const hymba_layer_cfg* cfg) {
 }
 
 // RoPE and append of the new tokens from in_proj's split-K slices, the page selection, and the
-// attention into o [B, Hq*D] fp32, on `st`.  The append clears the attention's counters: the
-// workspace serves other calls in between.
+// attention into o [B, Hq*D] fp32, on `st`.
 int launch_paged_decode(const PagedDecode& d, const hymba_layer_cfg* cfg, const Dims& m, int B, const int* positions,
                         const float* proj, int n_slices, bool own_kv, const PagedDecodeWs& L, uint8_t* ws, float* o,
                         const DeviceInfo& dev, cudaStream_t st) {
@@ -362,8 +357,8 @@ int launch_paged_decode(const PagedDecode& d, const hymba_layer_cfg* cfg, const 
   ap.table = t->pages; ap.table_stride = t->stride; ap.width = t->width;
   ap.B = ap.T = B;
   ap.G = m.Hq / m.Hkv;
-  ap.clear = reinterpret_cast<unsigned*>(ws + L.arrived);
-  ap.n_clear = PA_MAX_GRID;
+  ap.clear = status->parts;
+  ap.n_clear = PA_PART_WORDS;
   ap.status = status;
   HY_TRY(launch_paged_append(d.kv, ap, cfg->rope_base, dev.sms, st));
   if (d.top_pages > 0) {
@@ -392,7 +387,6 @@ int launch_paged_decode(const PagedDecode& d, const hymba_layer_cfg* cfg, const 
   p.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)m.D));
   p.status = status;
   PagedWs aw;
-  aw.arrived = L.arrived;
   aw.part = L.part;
   aw.total = L.total;
   return launch_paged_attn(d.kv, p, ws, aw, dev.sms, st);

@@ -161,8 +161,7 @@ const char* hymba_last_error(void);
 int hymba_mixer_workspace_size(const hymba_layer_cfg* cfg, int batch, int n_tokens, int x_has_meta, int mode,
                                size_t* bytes);
 
-/* Zero the status word of a workspace, and what follows it up to 4096 bytes (call once after
- * allocating it). */
+/* Zero the status word of a workspace, its first 256 bytes (call once after allocating it). */
 int hymba_workspace_init(void* workspace, size_t ws_bytes, hymba_stream stream);
 
 /* Synchronise `stream`, copy the workspace status word to *status and clear it.  *status is
@@ -336,9 +335,9 @@ typedef struct hymba_page_table {
 
 /* Bytes of workspace that hymba_paged_select and hymba_paged_attention need for up to `batch`
  * sequences of up to max_pages pages each (the table's width).  One workspace serves all the
- * paged calls, one after another; calls that may overlap on the GPU need one each.  The
- * attention keeps counters in it that hymba_workspace_init zeroes and every call leaves at
- * zero: a workspace that another kind of call has used in between must be initialised again. */
+ * paged calls, and calls of other kinds, one after another; calls that may overlap on the GPU need
+ * one each.  The attention keeps counters in the status word's 256 bytes, which
+ * hymba_workspace_init zeroes and every call leaves at zero. */
 int hymba_paged_workspace_size(const hymba_paged_kv* kv, int batch, int n_q_heads, int max_pages, size_t* bytes);
 
 /* Append new tokens: rotate (RoPE, half-split pairs, angle position * base^(-2j/D)) and store.

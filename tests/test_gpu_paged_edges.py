@@ -28,3 +28,33 @@ def test_meta_count_up_to_the_largest_int(M, W):
     got, lse, status = run_attention(k, v, table, lens, q, n_meta=M, window=W)
     assert status == H.OK
     check_attention(got, lse, ref, v, max(lens), dt, torch.float32, D)
+
+
+def test_workspace_init_leaves_what_lies_behind_the_status():
+    """hymba_workspace_init zeroes the status word's 256 bytes; a live workspace keeps the rest."""
+    ws = H.alloc_workspace(8192)
+    ws.fill_(0xa5)
+    H.check(H.lib().hymba_workspace_init(H.ptr(ws), ws.numel(), H.stream_handle(None)))
+    torch.cuda.synchronize()
+    assert (ws[:256] == 0).all() and (ws[256:] == 0xa5).all()
+
+
+def test_attention_after_other_calls_on_its_workspace():
+    """Whatever other calls leave behind the status word, the attention joins the parts of a
+    sequence that is cut over many CTAs; reading the status in between changes nothing."""
+    lens, ps, Hq, Hkv, D, dt = [9000, 40], 64, 10, 2, 64, torch.float16
+    k, v, table = R.make_pool(lens, ps, Hkv, D, dt, seed=92)
+    cache = H.PagedCache(k.cuda(), v.cuda())
+    q = torch.randn(2, Hq, D, generator=torch.Generator().manual_seed(93)).to(dt).cuda()
+    ln = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    ws = H.alloc_workspace(H.paged_workspace_size(cache, 2, Hq, table.shape[1]))
+    want = torch.empty(2, Hq, D, device="cuda")
+    H.paged_attention(cache, q, table.cuda(), ln, want, ws)
+    assert H.status_read(ws) == H.OK
+    for fill in (0xff, 0x01, 0x5a):
+        ws[256:] = fill          # as any call may that keeps its buffers there
+        got = torch.full_like(want, -7.0)
+        H.paged_attention(cache, q, table.cuda(), ln, got, ws)
+        assert H.status_read(ws) == H.OK
+        assert torch.equal(got, want), hex(fill)
+        assert (ws[:256] == 0).all()
