@@ -433,6 +433,9 @@ int hymba_paged_append(const hymba_paged_kv* kv, const hymba_page_table* table, 
     if (r.p != nullptr && (!aligned16(r.p) || r.s < r.w || r.s % vec))
       return fail(HYMBA_ERR_INVALID_ARG, "%s rows: not 16-byte aligned, or stride %lld", r.n, r.s);
   if (!aligned16(q_out)) return fail(HYMBA_ERR_INVALID_ARG, "q_out not 16-byte aligned");
+  if (q != nullptr && q == q_out &&
+      (src_dtype != kv->dtype || (n_tokens > 1 && q_stride != (long long)n_q_heads * kv->head_dim)))
+    return fail(HYMBA_ERR_INVALID_ARG, "queries in place: of another type than the pool, or rows not contiguous");
   DeviceInfo* dev = nullptr;
   HY_TRY(device_info(&dev));
   if (n_tokens == 0) return HYMBA_OK;

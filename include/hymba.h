@@ -353,7 +353,8 @@ int hymba_paged_workspace_size(const hymba_paged_kv* kv, int batch, int n_q_head
  *             q_stride elements apart (column slices of a fused projection): 16-byte aligned,
  *             strides multiples of 16 bytes.  k and v may be NULL together (only queries are
  *             rotated: a layer that reads another layer's cache), q and q_out likewise
- *   q_out     [n_tokens, Hq, D] in the pool's type; may be q itself (same type, rows contiguous)
+ *   q_out     [n_tokens, Hq, D] in the pool's type; may be q itself (same type, rows contiguous:
+ *             refused otherwise), and must not overlap the rows in any other way
  *   rope_base 0: no rotation (keys that were rotated before, e.g. a prefill cache's)
  * Page bounds, when the cache has them: a page whose row 0 is written in this call starts
  * over; otherwise the new keys widen its bounds.
