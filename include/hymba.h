@@ -395,9 +395,11 @@ int hymba_paged_select(const hymba_paged_kv* kv, const hymba_page_table* table, 
  *                             hymba_paged_select writes them: the first min(top_pages, pages of
  *                             the sequence) entries are read, entries that are no page of the
  *                             sequence are skipped, an entry listed twice counts twice)
- * A sequence with no visible position gets zeros.  Values and keys at positions that are not
- * visible, NaN included, have no influence; a visible NaN key makes the rows of its
- * group's heads NaN, a visible value that is not finite its channel in them NaN or infinite.
+ * A sequence with no visible position gets zeros, and so does a head for which every visible
+ * score is -inf (the formula's 0 / 0; lse is -inf in both cases).  Values and keys at positions
+ * that are not visible, NaN included, have no influence; a visible NaN key makes the rows of its
+ * group's heads NaN, a score of +inf its head's row, a visible value that is not finite its channel
+ * in them NaN or infinite.
  *   q    rows of n_q_heads * D in the pool's type (n_q_heads up to 16 per KV head), q_stride
  *        apart (a multiple of 8); out likewise in out_dtype (F32, BF16 or F16), rounded once,
  *        not overlapping q

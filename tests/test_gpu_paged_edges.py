@@ -58,3 +58,28 @@ def test_attention_after_other_calls_on_its_workspace():
         assert H.status_read(ws) == H.OK
         assert torch.equal(got, want), hex(fill)
         assert (ws[:256] == 0).all()
+
+
+@pytest.mark.parametrize("Hq,Hkv,D,dt", [(10, 2, 64, torch.float16), (12, 1, 64, torch.bfloat16),
+                                         (4, 1, 128, torch.bfloat16), (16, 1, 128, torch.float16)])
+def test_rows_whose_every_score_is_infinite(Hq, Hkv, D, dt):
+    """Keys of -inf in channel 0: a head with a positive query there scores -inf everywhere and
+    gets zeros and an lse of -inf, one with a negative query scores +inf and gets NaN; a head of
+    query 0 in that channel has 0 * inf.  The other sequences are as without them.  One sequence
+    within a tile, one cut over many CTAs."""
+    lens, ps = [40, 20000, 0, 130], 64
+    k, v, table = R.make_pool(lens, ps, Hkv, D, dt, seed=94)
+    q = torch.randn(len(lens), Hq, D, generator=torch.Generator().manual_seed(95)).to(dt)
+    q[:, :, 0] = 1.0
+    q[:, 1, 0] = -1.0
+    q[:, 2, 0] = 0.0
+    want, wl, _ = run_attention(k, v, table, lens, q)
+    for b in (0, 1):
+        for j in range(-(-lens[b] // ps)):
+            k[table[b, j], :, :, 0] = -float("inf")
+    got, lse, status = run_attention(k, v, table, lens, q)
+    assert status == H.OK
+    low = [h for h in range(Hq) if h not in (1, 2)]
+    assert (got[:2, low] == 0).all() and (lse[:2, low] == -float("inf")).all()
+    assert got[:2, 1:3].isnan().all() and lse[:2, 1:3].isnan().all()
+    assert torch.equal(got[2:], want[2:]) and torch.equal(lse[2:], wl[2:])
