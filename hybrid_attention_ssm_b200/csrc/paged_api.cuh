@@ -5,6 +5,7 @@
 namespace {
 
 constexpr int PAGED_MAX_SELECT_WIDTH = 16384;   // one CTA ranks a sequence's pages in shared memory
+constexpr int PSEL_TWO_PER_SM_WIDTH = 14000;    // up to here two such CTAs fit into an SM's shared memory
 
 struct PagedWs {
   size_t part, total;
@@ -258,12 +259,7 @@ int launch_paged_select(const hymba_paged_kv* kv, PagedSelectParams& p, cudaStre
   p.n_pages = kv->n_pages;
   p.ps_log2 = log2_int(kv->page_size);
   p.cap = paged_cap(p.width, kv->page_size);
-  // the largest cluster that leaves the CTAs of the call resident at once (four per SM) and at
-  // least 64 pages to a CTA
   const long long lists = (long long)p.B * p.Hkv;
-  int cluster = 8;
-  while (cluster > 1 && (lists * cluster > 4 * 148 || p.width < 64 * cluster)) cluster >>= 1;
-  if (lists * cluster > 0x7fffffff) return fail(HYMBA_ERR_UNSUPPORTED, "batch too large");
   return paged_dispatch(kv, [&](auto e, auto d) {
     auto kern = paged_select_kernel<decltype(e), decltype(d)::value>;
     static bool attr[64] = {false};
@@ -273,6 +269,45 @@ int launch_paged_select(const hymba_paged_kv* kv, PagedSelectParams& p, cudaStre
       HY_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, PAGED_MAX_SELECT_WIDTH * 8));
       attr[dcur & 63] = true;
     }
+    // CTAs of a cluster share a list's pages; what they cannot share (the start, the ranking) makes
+    // larger clusters worth less the shorter the lists are, and clusters that the device does not
+    // hold at once come in a second wave.  So: the largest cluster that leaves at least 64 pages to a
+    // CTA, while no more than n + n width / 4096 of them are needed, n being what the device holds:
+    // 33, 71 and 148 clusters of 8, 4 and 2 on a B200 (two CTAs per SM), half of that for tables of
+    // more than 14000 pages (the keys of the widest take 128 KB of every CTA's SM), and at most two
+    // such waves, or four of the halves.  Measured (us, all lists full | lengths spread):
+    //   lists x pages    of 8            of 4            of 2            of 1
+    //    60 x  1024      17.4 |  15.8    11.7 |  11.2    12.2 |  12.0    16.9 |  16.6
+    //   100 x  1024      23.8 |  22.0    17.9 |  16.0    15.0 |  14.6    17.1 |  18.5
+    //   240 x  1024      52.8 |  42.4    38.4 |  28.7    32.3 |  24.3    26.0 |  21.7
+    //    42 x  4096      31.5 |  22.3    29.4 |  24.3    37.4 |  32.1    63.7 |  49.3
+    //   100 x  4096      56.8 |  43.6    51.8 |  40.4    48.4 |  44.9    69.0 |  69.5
+    //   180 x  4096      92.3 |  67.3    81.0 |  57.3    88.0 |  56.5    83.1 |  77.4
+    //    36 x 15000     116   |  76.7   134   |  79.0   132   | 130     232   | 231
+    static std::atomic<int> resident[64][2][4];   // by device, table class, log2 of the cluster: 0 not asked yet
+    const int wide = p.width > PSEL_TWO_PER_SM_WIDTH ? 1 : 0;
+    int cluster = 8;
+    for (int l = 3; cluster > 1; --l, cluster >>= 1) {
+      if (p.width < 64 * cluster) continue;
+      int n = resident[dcur & 63][wide][l].load(std::memory_order_relaxed);
+      if (n == 0) {
+        cudaLaunchAttribute dim{};
+        dim.id = cudaLaunchAttributeClusterDimension;
+        dim.val.clusterDim.x = cluster;
+        dim.val.clusterDim.y = dim.val.clusterDim.z = 1;
+        cudaLaunchConfig_t q{};
+        q.gridDim = dim3((unsigned)cluster);
+        q.blockDim = dim3(PSEL_THREADS);
+        q.dynamicSmemBytes = (size_t)(wide ? PAGED_MAX_SELECT_WIDTH : PSEL_TWO_PER_SM_WIDTH) * 8;
+        q.attrs = &dim;
+        q.numAttrs = 1;
+        HY_CUDA(cudaOccupancyMaxActiveClusters(&n, kern, &q));
+        n = std::max(n, 1);
+        resident[dcur & 63][wide][l].store(n, std::memory_order_relaxed);
+      }
+      if (lists <= n + std::min((long long)n * p.width / 4096, (long long)n * (wide ? 3 : 1))) break;
+    }
+    if (lists * cluster > 0x7fffffff) return fail(HYMBA_ERR_UNSUPPORTED, "batch too large");
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)(lists * cluster));
     cfg.blockDim = dim3(PSEL_THREADS);

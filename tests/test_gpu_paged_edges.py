@@ -5,7 +5,7 @@ import torch
 
 from hybrid_attention_ssm_b200 import hymba as H
 from tests import paged_ref as R
-from tests.test_gpu_paged import check_attention, run_attention
+from tests.test_gpu_paged import check_attention, run_attention, run_select
 
 pytestmark = pytest.mark.gpu
 
@@ -83,3 +83,23 @@ def test_rows_whose_every_score_is_infinite(Hq, Hkv, D, dt):
     assert (got[:2, low] == 0).all() and (lse[:2, low] == -float("inf")).all()
     assert got[:2, 1:3].isnan().all() and lse[:2, 1:3].isnan().all()
     assert torch.equal(got[2:], want[2:]) and torch.equal(lse[2:], wl[2:])
+
+
+@pytest.mark.parametrize("B,Hkv,width", [(6, 5, 640), (12, 5, 640), (20, 5, 640), (45, 4, 640), (1, 2, 15000), (20, 1, 14001)])
+def test_select_with_clusters_of_every_size(B, Hkv, width):
+    """Numbers of lists and table widths between which the size of the cluster that serves a list
+    changes; full and short lists side by side."""
+    ps, D, dt, top = 16, 64, torch.float16, 24
+    g = torch.Generator().manual_seed(96)
+    n_pages = 700
+    mid, wid = torch.randn(n_pages, Hkv, D, generator=g), torch.rand(n_pages, Hkv, D, generator=g)
+    lo, hi = (mid - wid).to(dt), (mid + wid).to(dt)
+    pages = [width if b % 2 == 0 else 1 + (width * b) // B for b in range(B)]
+    table = torch.randint(0, n_pages, (B, width), generator=g).to(torch.int32)
+    q = torch.randn(B, 2 * Hkv, D, generator=g).to(dt)
+    got, status = run_select(lo, hi, table, [n * ps for n in pages], q, ps, top, 2, 1)
+    assert status == H.OK
+    for b, n in enumerate(pages):
+        every = R.scores(lo, hi, torch.arange(n_pages), q[b])[:, table[b, :n].long()]
+        for h in range(Hkv):
+            assert got[b, h].tolist() == R.select(every[h].tolist(), 2, 1, top), (b, h)
