@@ -1152,8 +1152,10 @@ __device__ __forceinline__ void pa_finish(const PagedAttnParams& p, int item, in
   const int b = item / p.Hkv, h = item % p.Hkv * p.G + hh;
   const float inv = pa_inverse(a.l);
   const long long at = b * p.out_stride + (long long)h * D + 4 * quad;
-  store_pair(p.out, p.out_dt, at, a.x[0] * inv, a.x[1] * inv);
-  store_pair(p.out, p.out_dt, at + 2, a.x[2] * inv, a.x[3] * inv);
+  const float y[4] = {a.x[0] * inv, a.x[1] * inv, a.x[2] * inv, a.x[3] * inv};
+  if (p.out_dt == PDT_F16) f16_range_guard<4>(y, p.status, 609);
+  store_pair(p.out, p.out_dt, at, y[0], y[1]);
+  store_pair(p.out, p.out_dt, at + 2, y[2], y[3]);
   if (p.lse != nullptr && quad == 0) p.lse[(long long)b * p.Hq + h] = pa_lse(a.m, a.l);
 }
 

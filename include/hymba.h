@@ -51,7 +51,8 @@ enum {
   HYMBA_ERR_CUDA = 4,         /* a CUDA runtime/driver call failed (message has details) */
   HYMBA_ERR_TIMEOUT = 5,      /* status word: a device-side bounded wait gave up */
   HYMBA_ERR_FP16_RANGE = 6,   /* status word: a value stored in fp16 (queries, keys, values, the
-                                 KV cache, FFN activations) had |v| >= 65520 and became +-inf */
+                                 KV cache, FFN activations, the paged attention's output) had
+                                 |v| >= 65520 and became +-inf */
 };
 
 enum { HYMBA_KV_OWN = 0, HYMBA_KV_PRODUCER = 1, HYMBA_KV_CONSUMER = 2 };
@@ -409,7 +410,8 @@ int hymba_paged_select(const hymba_paged_kv* kv, const hymba_page_table* table, 
  * scheduling.  Work is shared out on the device from seq_lens, so a captured call serves any
  * later lengths that the table can hold; they must not change while the call runs.
  * A length that is negative or beyond the table is recorded (HYMBA_ERR_INVALID_ARG) and
- * clamped; the positions of a page that is not in the pool are recorded and skipped. */
+ * clamped; the positions of a page that is not in the pool are recorded and skipped; an F16
+ * output that the type cannot hold is recorded (HYMBA_ERR_FP16_RANGE). */
 int hymba_paged_attention(const hymba_paged_kv* kv, const hymba_page_table* table, const int* seq_lens, const void* q,
                           long long q_stride, int n_q_heads, float scale, int n_meta, int window, const int* page_idx,
                           int top_pages, void* out, int out_dtype, long long out_stride, float* lse, void* workspace,

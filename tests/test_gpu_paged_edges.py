@@ -103,3 +103,24 @@ def test_select_with_clusters_of_every_size(B, Hkv, width):
         every = R.scores(lo, hi, torch.arange(n_pages), q[b])[:, table[b, :n].long()]
         for h in range(Hkv):
             assert got[b, h].tolist() == R.select(every[h].tolist(), 2, 1, top), (b, h)
+
+
+def test_fp16_outputs_out_of_range_are_recorded():
+    """A bf16 pool's values may lie beyond fp16: the output is infinite there, and the status says
+    so; in the other types, and with values that fit, it stays clear."""
+    dt = torch.bfloat16
+    k, v, table = R.make_pool([40, 9000], 64, 2, 64, dt, seed=97)
+    q = torch.randn(2, 10, 64, generator=torch.Generator().manual_seed(98)).to(dt)
+    big = v.clone()
+    big[table[0, 0].long(), 1, :, 7] = 1e5          # one channel of one kv head, in every row of its page
+    for b in range(2):
+        if b:                                       # and the same in the sequence that is cut and joined
+            big[table[1, :141].long(), 1, :, 7] = 1e5
+        got, _, status = run_attention(k, big, table, [40, 9000], q, torch.float16)
+        assert status == H.ERR_FP16_RANGE
+        for s in range(2):
+            assert torch.equal(got[s].isinf(), (torch.zeros(10, 64) + (0 if s > b else 1)).bool() &
+                               (torch.arange(10) >= 5)[:, None] & (torch.arange(64) == 7))
+    for vals, out_dt in ((big, torch.bfloat16), (big, torch.float32), (v, torch.float16)):
+        got, _, status = run_attention(k, vals, table, [40, 9000], q, out_dt)
+        assert status == H.OK and got.isfinite().all()
