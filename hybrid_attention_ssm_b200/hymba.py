@@ -599,11 +599,17 @@ def mixer_decode_paged(dims, dw: DeviceWeights, x, positions, cache: PagedCache,
                                        if t is not None])
     cfg = make_cfg(dims) if cfg is None else cfg
     tb, B, pos = _batch(table, positions, "positions")
-    if x.shape != (B, dims.d_model) or out.shape != x.shape or not (x.is_contiguous() and out.is_contiguous()):
-        _refuse("x and out must be contiguous [batch, d_model]")
+    if x.shape != (B, dims.d_model) or out.shape != x.shape:
+        _refuse("x and out must be [batch, d_model]")
+    for t, dt, n in ((x, torch.bfloat16, x.numel()), (out, torch.bfloat16, x.numel()),
+                     (residual, torch.bfloat16, x.numel()), (ssm_state, torch.float32, B * dims.d_inner * dims.d_state),
+                     (conv_state, torch.float32, B * dims.d_inner * (dims.d_conv - 1))):
+        if t is not None and not (t.dtype is dt and t.numel() >= n and t.is_contiguous()):
+            _refuse("x, out and residual must be contiguous bf16 [batch, d_model], ssm_state and conv_state contiguous "
+                    "fp32 [batch, d_inner, d_state] and [batch, d_inner, d_conv - 1]")
     check(lib().hymba_mixer_decode_paged(ctypes.byref(cfg), ctypes.byref(dw.c), ptr(x), pos, cache.ref,
-                                         ctypes.byref(tb), top_pages, ptr(ssm_state), ptr(conv_state), ptr(residual), ptr(out), ptr(ws),
-                                         ws.numel(), st))
+                                         ctypes.byref(tb), top_pages, ptr(ssm_state), ptr(conv_state), ptr(residual),
+                                         ptr(out), ptr(ws), ws.numel(), st))
 
 
 def mixer_decode_noalloc(dims, dw: DeviceWeights, x, position, kv: Cache, ssm_state, conv_state, out,
