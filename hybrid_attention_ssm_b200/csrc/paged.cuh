@@ -660,7 +660,8 @@ __global__ void __launch_bounds__(PAP_THREADS, PAP_PER_SM)
 //   score(page) = sum_d up_d hi_d + dn_d lo_d,   up_d = sum_h max(q_hd, 0), dn_d = sum_h min(q_hd, 0)
 // so a group costs one pair of dot products whatever G is.
 //
-// Ranks must not depend on rounding, so the scores are held in 64 bits.  A 16-bit value is put
+// The scores are held in 64 bits, so that ranks depend on rounding only where scores agree to
+// about 15 digits.  A 16-bit value is put
 // into a double by moving its bits (sign, exponent and mantissa, the exponent not rebiased):
 // that is the value times 2^(bias - 1023) exactly, subnormals included, at two integer
 // operations instead of a conversion; up and dn carry the inverse scale up to a factor that is
@@ -1017,10 +1018,14 @@ __global__ void __launch_bounds__(PSEL_THREADS, 2)
 // Bound by the keys' and values' bytes, read once (ncu: 310 MB for 307).  Long runs stream at
 // 6.6 TB/s (2.7 GB in 410 us; a plain copy reaches 6.55), to which a call adds about 10 us: 3 to
 // the first copy, 2 to its data, the spread of the SMs at the end, and 3 to publish and join
-// cut items.  Back to back, 8 x 65537 keys in bf16 take 99 us (floor 88), 64 x up to 8320 57
-// (47), one sequence of 131073 37 (26), a window of 1024 + 128 for 64 sequences 24 (15), 48
-// listed pages of 32 for 64 30 (18).  A fourth stage or two groups of five changed nothing or
-// cost 3%; two stages are 3% slower at D = 64 and 1% faster at D = 128.
+// cut items.  Back to back, with inputs that change from call to call, 8 x 65537 keys in bf16
+// take 101 us (floor 88), 64 x up to 8320 58 (47), one sequence of 131073 37 (26), a window of
+// 1024 + 128 for 64 sequences 28 (15), 48 listed pages of 32 for 64 32 (18).  A fourth stage or two
+// groups of five changed nothing or cost 3%; two stages are 3% slower at D = 64 and 1% faster
+// at D = 128.  9 to 16 heads per kv head are bound by the latency of the consumer warps' own
+// chains, of which fewer fit (255 registers a thread at D = 128, one consumer warp per scheduler:
+// issue slots 22% busy, DRAM 38%): 8 x up to 131073 keys, 16 heads x 64, 42 us in fp16 and 45 in bf16
+// (floor 22; 8 heads 35), 8 x up to 65537, 32/2 heads x 128, 78 and 88 us (44; 16/2 heads 56).
 // ----------------------------------------------------------------------------------------
 constexpr int PA_KT = 64;
 constexpr int PA_MAX_GRID = 148;   // CTAs (sizes the workspace)

@@ -373,8 +373,8 @@ int hymba_paged_append(const hymba_paged_kv* kv, const hymba_page_table* table, 
  * pages (they hold the meta tokens), the last n_last (the newest tokens), and of the others
  * those with the largest
  *   score(page) = sum over the group's query heads of max { q . k : k_lo <= k <= k_hi },
- * top_pages in all, ties to the lower page number.  Scores are held in 64 bits, so the choice
- * does not depend on rounding.
+ * top_pages in all, ties to the lower page number.  Scores are held in 64 bits: the choice
+ * depends on rounding only between scores that agree to about 15 digits.
  *   seq_lens  int32 [batch] (device): positions in the cache, the new token's included
  *   q         [batch] rows of n_q_heads * D in the pool's type, q_stride apart, rotated
  *   page_idx  int32 [batch, Hkv, top_pages] (device, output): numbers within the sequence,
