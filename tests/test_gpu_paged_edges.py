@@ -1,5 +1,7 @@
 """The paged cache operators at the ends of what their arguments may be, against the 64-bit
 definitions in paged_ref; bounds as derived in test_gpu_paged."""
+import threading
+
 import pytest
 import torch
 
@@ -124,3 +126,51 @@ def test_fp16_outputs_out_of_range_are_recorded():
     for vals, out_dt in ((big, torch.bfloat16), (big, torch.float32), (v, torch.float16)):
         got, _, status = run_attention(k, vals, table, [40, 9000], q, out_dt)
         assert status == H.OK and got.isfinite().all()
+
+
+def test_select_captured_and_from_several_threads():
+    """A selection served by clusters, captured into a graph, and called from several host threads on
+    streams and workspaces of their own: what the first eager call of a process asks CUDA about
+    the device must not matter to either."""
+    dt, D, Hkv, B, width, top = torch.bfloat16, 128, 4, 12, 700, 20
+    g = torch.Generator().manual_seed(99)
+    lo = torch.randn(800, Hkv, D, generator=g).to(dt)
+    hi = lo + torch.rand(800, Hkv, D, generator=g).to(dt)
+    k = torch.zeros(800, Hkv, 16, D, dtype=dt, device="cuda")
+    cache = H.PagedCache(k, k, lo.cuda(), hi.cuda())
+    table = torch.randint(0, 800, (B, width), generator=g).to(torch.int32)
+    q = torch.randn(B, 8, D, generator=g).to(dt)
+    lens = torch.full((B,), width * 16, dtype=torch.int32, device="cuda")
+    tb, qg = table.cuda(), q.cuda()
+    res = [torch.full((B, Hkv, top), 77, dtype=torch.int32, device="cuda") for _ in range(5)]
+    wss = [H.alloc_workspace(256) for _ in range(5)]
+    torch.cuda.synchronize()
+    graph, st = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    with torch.cuda.stream(st), torch.cuda.graph(graph, stream=st):
+        H.paged_select(cache, qg, tb, lens, res[0], wss[0])
+    graph.replay()
+    errors = []
+
+    def work(i):
+        try:
+            s = torch.cuda.Stream()
+            for _ in range(20):
+                H.paged_select(cache, qg, tb, lens, res[i], wss[i], stream=s)
+            s.synchronize()
+        except Exception as e:   # a failure in a thread must reach the test
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(1, 5)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not errors and all(H.status_read(w) == H.OK for w in wss)
+    for r in res[1:]:
+        assert torch.equal(r, res[0])
+    got = res[0].cpu()
+    for b in range(B):
+        sc = R.scores(lo, hi, table[b], q[b])
+        for h in range(Hkv):
+            assert got[b, h].tolist() == R.select(sc[h].tolist(), 1, 1, top)
